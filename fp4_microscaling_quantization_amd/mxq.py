@@ -21,10 +21,14 @@ LAYOUT_ROWS, LAYOUT_MFMA = 0, 1
 AXIS_ROW, AXIS_COL = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 SIGNS_MASK, SIGNS_PER_BLOCK = 0, 1
+NORM_LAYER, NORM_RMS = 0, 1
+TOP_MAX = 64
 
 SYMBOLS = ("mxq_quantize", "mxq_quantize_batch", "mxq_dequantize", "mxq_wgrad_gemm", "mxq_gemm_abt", "mxq_bias_stats",
            "mxq_bias_stats_workspace_size", "mxq_bias_stats_noalloc", "mxq_bucket_ratio", "mxq_round_to_grid", "mxq_rht_sign_mask", "mxq_rotate",
-           "mxq_status_string", "mxq_abi_version")
+           "mxq_norm_forward", "mxq_norm_backward", "mxq_norm_backward_workspace_size", "mxq_token_logprobs",
+           "mxq_token_logprobs_backward", "mxq_vocab_workspace_size", "mxq_distill_forward",
+           "mxq_distill_backward", "mxq_distill", "mxq_status_string", "mxq_abi_version")
 
 
 class QConfig(C.Structure):
@@ -89,11 +93,29 @@ def lib() -> C.CDLL:
         L.mxq_round_to_grid.argtypes = [i32, i32, i32, P, P, i64, P, P]
         L.mxq_bucket_ratio.argtypes = [C.POINTER(Stats), i32]
         L.mxq_bucket_ratio.restype = C.c_double
+        sz, f32 = C.c_size_t, C.c_float
+        L.mxq_norm_forward.argtypes = [i32, P, i32, i64, i64, i64, P, P, f32, P, i32, i64, P, P, P]
+        L.mxq_norm_backward.argtypes = [i32, P, i32, i64, P, i32, i64, i64, i64, P, P, P, P, i32,
+                                        i64, P, P, P, sz, P]
+        L.mxq_norm_backward_workspace_size.argtypes = [i64, i64]
+        L.mxq_norm_backward_workspace_size.restype = sz
+        logits = [P, i32, i64, i64, i64, f32]
+        teacher = [P, P, i32, i32, P]
+        L.mxq_token_logprobs.argtypes = logits + [P, P, P, P, i32, P, P, P, sz, P]
+        L.mxq_token_logprobs_backward.argtypes = logits + [P, P, P, P, P, P, i32, i64, P]
+        L.mxq_vocab_workspace_size.argtypes = [i64, i64, i32]
+        L.mxq_vocab_workspace_size.restype = sz
+        L.mxq_distill_forward.argtypes = logits + teacher + [P, P, P, sz, P]
+        L.mxq_distill_backward.argtypes = logits + teacher + [P, P, i32, i64, P]
+        L.mxq_distill.argtypes = logits + teacher + [P, P, i32, i64, P, sz, P]
         L.mxq_status_string.argtypes = [i32]
         L.mxq_status_string.restype = C.c_char_p
         L.mxq_abi_version.restype = i32
         for name in ("mxq_quantize", "mxq_quantize_batch", "mxq_dequantize", "mxq_wgrad_gemm", "mxq_gemm_abt",
-                     "mxq_bias_stats", "mxq_bias_stats_noalloc", "mxq_round_to_grid", "mxq_rotate"):
+                     "mxq_bias_stats", "mxq_bias_stats_noalloc", "mxq_round_to_grid", "mxq_rotate",
+                     "mxq_norm_forward", "mxq_norm_backward", "mxq_token_logprobs",
+                     "mxq_token_logprobs_backward", "mxq_distill_forward", "mxq_distill_backward",
+                     "mxq_distill"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -463,3 +485,210 @@ def round_to_grid(a, grid: int, round=RTNE, rand=None, sr_bits=16, out=None, str
     _check("mxq_round_to_grid", lib().mxq_round_to_grid(grid, round, sr_bits, _ptr(a), _ptr(rand),
                                                         n, _ptr(codes), _stream(stream)))
     return codes
+
+
+# ---- the operators around the products --------------------------------------
+# These take tensors of their own types and strides, so the binding checks what
+# the C entry points cannot see: a wrong element type, a stride along the row,
+# a vector of another length or a tensor elsewhere raises a ValueError.
+
+_DTYPES = None
+
+
+def _dtype(t) -> int:
+    """MXQ_OUT_* of a tensor or torch dtype."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+    code = _DTYPES.get(getattr(t, "dtype", t))
+    if code is None:
+        raise ValueError(f"float32 or bfloat16 expected, not {getattr(t, 'dtype', t)}")
+    return code
+
+
+def _matrix(name, t, like=None):
+    """(address, dtype code, leading dimension) of a 2-D tensor whose rows are contiguous."""
+    code = _dtype(t)
+    if t.dim() != 2 or (like is not None and t.shape != like.shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}" + (f", not {tuple(like.shape)}" if like is not None else " is not 2-D"))
+    rows, cols = t.shape
+    ld = t.stride(0)
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name}: rows must be contiguous and apart (strides {t.stride()})")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, not {like.device}")
+    return t.data_ptr(), code, ld if rows > 1 else max(ld, cols)
+
+
+def _vector(name, t, shape, like, dtype=None):
+    """Address of a packed fp32 (or `dtype`) tensor of this shape, None for None."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != (dtype or torch.float32) or tuple(t.shape) != shape or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name}: packed {dtype or torch.float32} of shape {shape} on {like.device} expected, "
+                         f"not {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+class _On:
+    """The device and stream of a call: outputs and workspaces are allocated on
+    the stream that uses them, so that their memory is not handed on early."""
+
+    def __init__(self, x, stream):
+        import torch
+        if not x.is_cuda:
+            raise ValueError("GPU tensors expected")
+        if x.device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+        self.torch, self.device, self.stream = torch, x.device, stream
+        self.handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.stream):
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, size):
+        """(tensor, address, bytes); the tensor has to live until the call is enqueued."""
+        if not size:
+            return None, None, 0
+        ws = self.empty((size,), self.torch.uint8)
+        return ws, ws.data_ptr(), size
+
+
+def norm_forward(x, gamma=None, beta=None, *, eps, kind=NORM_LAYER, out_dtype=None, out=None, stream=None):
+    """mxq_norm_forward: (y, mean, rstd); mean is None for NORM_RMS.  y has x's
+    dtype unless out_dtype says otherwise, or is `out` (x itself serves)."""
+    on = _On(x, stream)
+    f32 = on.torch.float32
+    rows, cols = x.shape
+    y = on.empty((rows, cols), out_dtype or x.dtype) if out is None else out
+    xp, xt, ldx = _matrix("x", x)
+    yp, yt, ldy = _matrix("out", y, x)
+    mean = on.empty((rows,), f32) if kind == NORM_LAYER else None
+    rstd = on.empty((rows,), f32)
+    _check("mxq_norm_forward", lib().mxq_norm_forward(
+        kind, xp, xt, ldx, rows, cols, _vector("gamma", gamma, (cols,), x),
+        _vector("beta", beta, (cols,), x), eps, yp, yt, ldy, _ptr(mean), _ptr(rstd), on.handle))
+    return y, mean, rstd
+
+
+def norm_backward(dy, x, gamma, mean, rstd, *, kind=NORM_LAYER, weight=True, bias=True, out_dtype=None,
+                  out=None, stream=None):
+    """mxq_norm_backward: (dx, dgamma, dbeta); dgamma without `weight` and dbeta
+    without `bias` are None.  dx has x's dtype unless out_dtype says otherwise,
+    or is `out` (dy or x itself serves)."""
+    on = _On(x, stream)
+    f32 = on.torch.float32
+    rows, cols = x.shape
+    dx = on.empty((rows, cols), out_dtype or x.dtype) if out is None else out
+    xp, xt, ldx = _matrix("x", x)
+    dp, dt, ldd = _matrix("dy", dy, x)
+    op, ot, ldo = _matrix("out", dx, x)
+    dgamma = on.empty((cols,), f32) if weight else None
+    dbeta = on.empty((cols,), f32) if bias else None
+    size = lib().mxq_norm_backward_workspace_size(rows, cols) if weight or bias else 0
+    ws, wp, size = on.workspace(size)
+    _check("mxq_norm_backward", lib().mxq_norm_backward(
+        kind, dp, dt, ldd, xp, xt, ldx, rows, cols, _vector("gamma", gamma, (cols,), x),
+        _vector("mean", mean if kind == NORM_LAYER else None, (rows,), x),
+        _vector("rstd", rstd, (rows,), x), op, ot, ldo, _ptr(dgamma), _ptr(dbeta), wp, size,
+        on.handle))
+    return dx, dgamma, dbeta
+
+
+def token_logprobs(logits, tokens=None, *, top_k=0, temperature=1, entropy=True, stream=None):
+    """mxq_token_logprobs: [logprob, entropy, stats], and top_ids, top_logprobs
+    after them where top_k > 0; logprob is None without tokens (int32), entropy
+    where it is not asked for."""
+    on = _On(logits, stream)
+    f32, i32 = on.torch.float32, on.torch.int32
+    rows, vocab = logits.shape
+    zp, zt, ld = _matrix("logits", logits)
+    out = [on.empty((rows,), f32) if tokens is not None else None,
+           on.empty((rows,), f32) if entropy else None, on.empty((rows, 2), f32)]
+    ids = lps = None
+    if top_k > 0:
+        ids, lps = on.empty((rows, top_k), i32), on.empty((rows, top_k), f32)
+    ws, wp, size = on.workspace(lib().mxq_vocab_workspace_size(rows, vocab, top_k))
+    _check("mxq_token_logprobs", lib().mxq_token_logprobs(
+        zp, zt, ld, rows, vocab, temperature, _vector("tokens", tokens, (rows,), logits, i32),
+        _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), top_k, _ptr(ids), _ptr(lps), wp, size, on.handle))
+    return out + [ids, lps] if top_k > 0 else out
+
+
+def token_logprobs_backward(logits, tokens, stats, entropy=None, d_logprob=None, d_entropy=None, *,
+                            temperature=1, out_dtype=None, out=None, stream=None):
+    """mxq_token_logprobs_backward: the gradient of the logits, in their dtype
+    unless out_dtype says otherwise, or in `out` (the logits themselves serve)."""
+    on = _On(logits, stream)
+    rows, vocab = logits.shape
+    o = on.empty((rows, vocab), out_dtype or logits.dtype) if out is None else out
+    zp, zt, ld = _matrix("logits", logits)
+    op, ot, ldo = _matrix("out", o, logits)
+    _check("mxq_token_logprobs_backward", lib().mxq_token_logprobs_backward(
+        zp, zt, ld, rows, vocab, temperature,
+        _vector("tokens", tokens, (rows,), logits, on.torch.int32),
+        _vector("stats", stats, (rows, 2), logits), _vector("entropy", entropy, (rows,), logits),
+        _vector("d_logprob", d_logprob, (rows,), logits),
+        _vector("d_entropy", d_entropy, (rows,), logits), op, ot, ldo, on.handle))
+    return o
+
+
+def _teacher_args(on, logits, ids, logprobs, weight, renormalize):
+    rows, top_k = logits.shape[0], ids.shape[-1]
+    return (_vector("teacher_ids", ids, (rows, top_k), logits, on.torch.int32),
+            _vector("teacher_logprobs", logprobs, (rows, top_k), logits), top_k,
+            1 if renormalize else 0, _vector("weight", weight, (rows,), logits))
+
+
+def distill_forward(logits, teacher_ids, teacher_logprobs, weight=None, *, temperature=1,
+                    renormalize=True, stream=None):
+    """mxq_distill_forward: (loss, stats)."""
+    on = _On(logits, stream)
+    rows, vocab = logits.shape
+    zp, zt, ld = _matrix("logits", logits)
+    loss, stats = on.empty((rows,), on.torch.float32), on.empty((rows, 2), on.torch.float32)
+    ws, wp, size = on.workspace(lib().mxq_vocab_workspace_size(rows, vocab, 0))
+    _check("mxq_distill_forward", lib().mxq_distill_forward(
+        zp, zt, ld, rows, vocab, temperature,
+        *_teacher_args(on, logits, teacher_ids, teacher_logprobs, weight, renormalize),
+        _ptr(loss), _ptr(stats), wp, size, on.handle))
+    return loss, stats
+
+
+def distill_backward(logits, teacher_ids, teacher_logprobs, stats, weight=None, *, temperature=1,
+                     renormalize=True, out_dtype=None, out=None, stream=None):
+    """mxq_distill_backward: the gradient of the logits, in their dtype unless
+    out_dtype says otherwise, or in `out` (the logits themselves serve)."""
+    on = _On(logits, stream)
+    rows, vocab = logits.shape
+    o = on.empty((rows, vocab), out_dtype or logits.dtype) if out is None else out
+    zp, zt, ld = _matrix("logits", logits)
+    op, ot, ldo = _matrix("out", o, logits)
+    _check("mxq_distill_backward", lib().mxq_distill_backward(
+        zp, zt, ld, rows, vocab, temperature,
+        *_teacher_args(on, logits, teacher_ids, teacher_logprobs, weight, renormalize),
+        _vector("stats", stats, (rows, 2), logits), op, ot, ldo, on.handle))
+    return o
+
+
+def distill(logits, teacher_ids, teacher_logprobs, weight=None, *, temperature=1, renormalize=True,
+            out_dtype=None, out=None, stream=None):
+    """mxq_distill: (loss, gradient of the logits) in one pass; the gradient as
+    in distill_backward."""
+    on = _On(logits, stream)
+    rows, vocab = logits.shape
+    o = on.empty((rows, vocab), out_dtype or logits.dtype) if out is None else out
+    zp, zt, ld = _matrix("logits", logits)
+    op, ot, ldo = _matrix("out", o, logits)
+    loss = on.empty((rows,), on.torch.float32)
+    ws, wp, size = on.workspace(lib().mxq_vocab_workspace_size(rows, vocab, 0))
+    _check("mxq_distill", lib().mxq_distill(
+        zp, zt, ld, rows, vocab, temperature,
+        *_teacher_args(on, logits, teacher_ids, teacher_logprobs, weight, renormalize),
+        _ptr(loss), op, ot, ldo, wp, size, on.handle))
+    return loss, o

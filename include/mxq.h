@@ -330,6 +330,130 @@ mxq_status mxq_round_to_grid(int32_t grid, int32_t round, int32_t sr_bits, const
  * stochastic-rounding stream uses.  Host function; returns 0 for other n. */
 uint32_t mxq_rht_sign_mask(uint64_t seed, uint32_t n);
 
+/* ---- the operators around the quantized products ---------------------------
+ * The norm before a linear layer (its output is what mxq_quantize takes, its
+ * backward pass takes mxq_gemm_abt's fp32 output), and the two ends of the
+ * output layer: log probabilities with alternatives, and the distillation
+ * loss.  No passage of the pages defines these; the formulas below do.
+ *  - Tensors are fp32 or bf16 per their own *_dtype argument (MXQ_OUT_F32 /
+ *    MXQ_OUT_BF16); all arithmetic is fp32, rounded once (nearest, ties to
+ *    even) where bf16 is stored.  Pointers must be aligned to their element
+ *    size only; leading dimensions (elements) may be any number >= the row length.
+ *  - rows == 0 launches nothing (mxq_norm_backward then clears dgamma and
+ *    dbeta), whatever the row pointers are.
+ *  - Sums run in a fixed order: repeated calls give the same bits. */
+#define MXQ_NORM_LAYER 0
+#define MXQ_NORM_RMS 1
+
+/* y = (x - mu) rstd gamma + beta for each row of x [rows x cols]:
+ *   MXQ_NORM_LAYER: mu the row's mean, rstd = 1 / sqrt(mean((x - mu)^2) + eps);
+ *   MXQ_NORM_RMS:   mu = 0,            rstd = 1 / sqrt(mean(x^2) + eps).
+ * gamma, beta (fp32 [cols]) may be NULL (1 and 0).  mean, rstd (fp32 [rows])
+ * may be NULL; they are what mxq_norm_backward takes (RMS writes no mean).
+ * cols >= 1, eps finite and >= 0.  y may be x itself (same dtype and leading
+ * dimension).  Rows that are not finite follow the formula in IEEE arithmetic
+ * and leave the others alone. */
+mxq_status mxq_norm_forward(int32_t kind, const void *x, int32_t x_dtype, int64_t ld_x,
+                            int64_t rows, int64_t cols, const float *gamma, const float *beta,
+                            float eps, void *y, int32_t y_dtype, int64_t ld_y, float *mean,
+                            float *rstd, void *stream);
+
+/* The backward pass of mxq_norm_forward from its mean (NULL for RMS) and rstd.
+ * With n = (x - mu) rstd and u = dy gamma, means over the row:
+ *   dx = rstd (u - n mean(u n) - mean(u))   (the last term for LAYER only);
+ *   dgamma = sum over rows of dy n,  dbeta = sum over rows of dy  (fp32 [cols],
+ *   each may be NULL; overwritten).
+ * dx may be NULL, or dy or x itself (same dtype and leading dimension).
+ * workspace: mxq_norm_backward_workspace_size(rows, cols) bytes, 4-byte
+ * aligned; needed only when dgamma or dbeta is asked for. */
+mxq_status mxq_norm_backward(int32_t kind, const void *dy, int32_t dy_dtype, int64_t ld_dy,
+                             const void *x, int32_t x_dtype, int64_t ld_x, int64_t rows,
+                             int64_t cols, const float *gamma, const float *mean,
+                             const float *rstd, void *dx, int32_t dx_dtype, int64_t ld_dx,
+                             float *dgamma, float *dbeta, void *workspace, size_t ws_bytes,
+                             void *stream);
+size_t mxq_norm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/* The softmax distribution q = softmax(z / temperature) of each row z of
+ * logits [rows x vocab], as m = max z and S = sum exp((z - m) / temperature):
+ *   logprob[r]  = log q at tokens[r] (int32; < 0: no token, 0 is written;
+ *                 >= vocab: NaN);
+ *   entropy[r]  = -sum q log q;
+ *   stats[r]    = (m, S), fp32 pairs, what the backward passes take;
+ *   top_ids, top_logprobs [rows x top_k]: the top_k largest logits in falling
+ *                 order, equal ones by index, and their log q.  0 <= top_k <= 64
+ *                 (MXQ_TOP_MAX).
+ * Outputs other than stats may be NULL (tokens with logprob; the top pair
+ * together, top_k then 0).  Logits of -inf are masked: they have q = 0, are no
+ * alternatives, and where fewer than top_k are left, the ids are -1 and their
+ * log q -inf.  A row with every logit masked has S = 0, entropy 0 and log q
+ * -inf.  A row that holds a NaN or +inf has no distribution: its floating
+ * outputs are NaN (stats: S), its ids -1.  1 <= vocab < 2^31, temperature finite
+ * and > 0.
+ * workspace: mxq_vocab_workspace_size(rows, vocab, top_k) bytes, 8-byte aligned
+ * (may be NULL where that is 0). */
+#define MXQ_TOP_MAX 64
+mxq_status mxq_token_logprobs(const void *logits, int32_t dtype, int64_t ld, int64_t rows,
+                              int64_t vocab, float temperature, const int32_t *tokens,
+                              float *logprob, float *entropy, float *stats, int32_t top_k,
+                              int32_t *top_ids, float *top_logprobs, void *workspace,
+                              size_t ws_bytes, void *stream);
+/* The workspace of mxq_token_logprobs, mxq_distill_forward and mxq_distill
+ * (those two: top_k = 0), in bytes; 0 for sizes they refuse. */
+size_t mxq_vocab_workspace_size(int64_t rows, int64_t vocab, int32_t top_k);
+
+/* The gradient of mxq_token_logprobs' logprob and entropy, from its stats and
+ * entropy and the gradients d_logprob, d_entropy [rows] (either may be NULL: 0;
+ * entropy and d_entropy go together, tokens and d_logprob too):
+ *   dz_v = (d_logprob (1[v = token] - q_v) - d_entropy q_v (log q_v + entropy)) / temperature
+ * into dlogits (all vocab columns of every row; may be logits itself, same
+ * dtype and leading dimension).  Token < 0: d_logprob counts as 0;
+ * token >= vocab: the row is NaN.  Masked logits have q = 0, rows without a
+ * distribution are NaN. */
+mxq_status mxq_token_logprobs_backward(const void *logits, int32_t dtype, int64_t ld,
+                                       int64_t rows, int64_t vocab, float temperature,
+                                       const int32_t *tokens, const float *stats,
+                                       const float *entropy, const float *d_logprob,
+                                       const float *d_entropy, void *dlogits,
+                                       int32_t dlogits_dtype, int64_t ld_dlogits, void *stream);
+
+/* Distillation from a teacher's top alternatives: top_k (1..MXQ_TOP_MAX) ids
+ * (int32, < 0: absent) and log probabilities (fp32) a row, packed [rows x
+ * top_k], as mxq_token_logprobs writes them at the same temperature.
+ * p_j = exp(teacher_logprobs_j), divided by their sum where renormalize is 1
+ * (then any logits / temperature serve); with q as above, P = sum p_j and
+ * weight w (fp32 [rows], NULL: 1):
+ *   loss[r] = w temperature^2 sum_j p_j (log p_j - log q at id_j)
+ *   dz_v    = w temperature (P q_v - sum over j with id_j = v of p_j),
+ * which is the gradient of the sum of the losses.  One certain alternative
+ * (top_k = 1, log probability 0) at temperature 1 is the cross entropy.
+ * A row with w = 0, or without a present alternative of p > 0, has loss 0 and
+ * gradient 0 whatever else it holds; an id >= vocab makes its row NaN.  An id may
+ * come twice.  Where a p > 0 meets a masked logit, the loss is +inf and the
+ * gradient finite.
+ *   mxq_distill_forward:  loss and stats (as mxq_token_logprobs writes them;
+ *                         rows of w = 0 get (0, 1)).
+ *   mxq_distill_backward: dlogits from stats; w then is the gradient of the
+ *                         unweighted loss.
+ *   mxq_distill:          loss and dlogits in one pass.
+ * dlogits may be logits itself (same dtype and leading dimension). */
+mxq_status mxq_distill_forward(const void *logits, int32_t dtype, int64_t ld, int64_t rows,
+                               int64_t vocab, float temperature, const int32_t *teacher_ids,
+                               const float *teacher_logprobs, int32_t top_k, int32_t renormalize,
+                               const float *weight, float *loss, float *stats, void *workspace,
+                               size_t ws_bytes, void *stream);
+mxq_status mxq_distill_backward(const void *logits, int32_t dtype, int64_t ld, int64_t rows,
+                                int64_t vocab, float temperature, const int32_t *teacher_ids,
+                                const float *teacher_logprobs, int32_t top_k,
+                                int32_t renormalize, const float *weight, const float *stats,
+                                void *dlogits, int32_t dlogits_dtype, int64_t ld_dlogits,
+                                void *stream);
+mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                       float temperature, const int32_t *teacher_ids,
+                       const float *teacher_logprobs, int32_t top_k, int32_t renormalize,
+                       const float *weight, float *loss, void *dlogits, int32_t dlogits_dtype,
+                       int64_t ld_dlogits, void *workspace, size_t ws_bytes, void *stream);
+
 /* Utilities (no passage defines them): a static description of a status
  * code, and the ABI version the library was built with (MXQ_ABI_VERSION). */
 const char *mxq_status_string(mxq_status s);
