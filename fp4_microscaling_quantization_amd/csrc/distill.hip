@@ -1,0 +1,450 @@
+// Distillation from a teacher's top alternatives (mxq_distill and its two
+// halves), and the gradient of token log probabilities (both have the form
+// dz = q (k0 + k1 d) apart from a few entries; include/mxq.h holds the formulas).
+//
+// mxq_distill with many rows is one pass: a workgroup holds its row in
+// registers (longer rows: the last stretch of it), so the logits come from
+// memory once and the gradient goes there once.  Everything else runs as
+// statistics of rows and a gradient of chunks.
+#include "vocab.hpp"
+
+namespace mxq {
+
+namespace {
+
+// ---- the teacher -------------------------------------------------------------------
+
+struct TeacherArgs {
+    const int32_t *ids;
+    const float *lps;
+    int32_t top_k, renormalize;
+    const float *weight;
+};
+
+// A row's teacher, one alternative per lane, the same in every wave: its id (-1:
+// absent), log p and p (0 where absent); their sum; whether an id is beyond the
+// vocabulary; whether some p is not 0.
+struct Teacher {
+    int id;
+    float p, logp, sum;
+    bool bad, used;
+};
+__device__ __forceinline__ Teacher teacher_row(const TeacherArgs &a, int64_t r, int vocab)
+{
+    const int lane = threadIdx.x & 63;
+    Teacher t;
+    t.id = lane < a.top_k ? a.ids[r * a.top_k + lane] : -1;
+    t.bad = __any(t.id >= vocab);
+    t.logp = t.id >= 0 ? a.lps[r * a.top_k + lane] : -INFINITY;
+    if (a.renormalize) {
+        const float m = base_of(wave_max(t.logp));
+        const float s = wave_sum(expf(t.logp - m));
+        if (s != 0.0f)
+            t.logp = t.logp - m - logf(s);
+    }
+    t.p = expf(t.logp);
+    t.sum = wave_sum(t.p);
+    t.used = __any(!(t.p == 0.0f));
+    return t;
+}
+__device__ __forceinline__ bool counts(const Teacher &t, float w)
+{
+    return w != 0.0f && (t.used || t.bad);
+}
+// the loss of a row that counts; zt: the student's logit at the lane's id
+__device__ __forceinline__ float row_loss(const Teacher &t, float zt, bool have, float w,
+                                          const RowStats &st, const Heat &h)
+{
+    const float term = have && t.p != 0.0f ? t.p * (t.logp - log_q(zt, st, h)) : 0.0f;
+    const float sum = wave_sum(term);
+    return t.bad ? NAN : w * (h.t * h.t * sum);
+}
+
+// ---- gradients -----------------------------------------------------------------------
+
+// dz = 2^d (k0 + k1 d), d = (z - b) log2 (in units of log2): what every entry of
+// a row has; the 1 / S, the weight and the temperature are in k0 and k1.
+struct Gradient {
+    float b, k0, k1;
+};
+template <bool SLOPE>
+__device__ __forceinline__ float gradient_at(float z, const Gradient &g, float log2)
+{
+    const float d = (z - g.b) * log2;
+    const float e = __builtin_amdgcn_exp2f(d);
+    return e * (SLOPE ? fmaf(g.k1, fmaxf(d, kFloorLog2), g.k0) : g.k0);
+}
+__device__ __forceinline__ Gradient distill_gradient(const Teacher &t, float w, const RowStats &st,
+                                                     const Heat &h)
+{
+    if (t.bad)
+        return {0.0f, NAN, 0.0f};
+    // a row with every logit masked: q = 0
+    return {base_of(st.m), st.s == 0.0f ? 0.0f : w * h.t * t.sum / st.s, 0.0f};
+}
+
+template <bool SLOPE, class T, class O, int NT, int NV>
+__device__ __forceinline__ void write_gradient(const Held<T, NT, NV> &held, O *o, int n,
+                                               const Gradient &g, float log2)
+{
+    constexpr int E = kElems<T>;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (held.any(i, n)) {
+            float f[E];
+            held.get(i, f);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                f[j] = gradient_at<SLOPE>(f[j], g, log2);
+            store_held<O, NT>(o, i, n, f);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// n entries at o, all `value`
+template <class O, int NT> __device__ __forceinline__ void write_all(O *o, int n, float value)
+{
+    constexpr int E = kElems<O>;
+    float f[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        f[j] = value;
+    for (int64_t at = (int)threadIdx.x * E; at < n; at += NT * E)
+        store_some(o + at, f, (int)(n - at));
+}
+
+// The entries of the teacher's ids in [from, to) once more, with their p: zt is the
+// logit there, loaded before the row was written (the gradient may lie over the
+// logits).  An id that comes twice: each of its lanes has the sum of both p and
+// writes the same value.  Called by one wave, after a barrier.
+template <class O>
+__device__ __forceinline__ void write_ids(O *o, const Teacher &t, float zt, int from, int to,
+                                          const Gradient &g, float wt, int top_k, float log2)
+{
+    float p = 0.0f;
+    for (int j = 0; j < top_k; ++j) {
+        const int id = __shfl(t.id, j);
+        const float pj = __shfl(t.p, j);
+        p += id == t.id ? pj : 0.0f;
+    }
+    if (t.id >= from && t.id < to)
+        o[t.id] = (O)fmaf(-wt, p, gradient_at<false>(zt, g, log2));
+}
+
+// ---- whole rows ----------------------------------------------------------------------
+
+// One workgroup per row: loss (stats where asked for), and with GRADIENT dlogits.
+// Rows longer than the registers hold: the stretches before the last are read
+// again for the gradient, from the last-level cache, where one row per CU stays.
+template <class T, class O, int NT, bool GRADIENT>
+__global__ void __launch_bounds__(NT, 4)
+k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, TeacherArgs ta,
+               float *loss, float *stats, O *dlogits, int64_t ld_o)
+{
+    using H = Held<T, NT, kHeld>;
+    __shared__ float lds[3 * NT / 64];
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T *z = logits + r * ld;
+        O *o = GRADIENT ? dlogits + r * ld_o : nullptr;
+        const float w = ta.weight ? ta.weight[r] : 1.0f;
+        if (w == 0.0f) {
+            if (threadIdx.x == 0) {
+                loss[r] = 0.0f;
+                if (stats) {
+                    stats[2 * r] = 0.0f;
+                    stats[2 * r + 1] = 1.0f;
+                }
+            }
+            if (GRADIENT)
+                write_all<O, NT>(o, vocab, 0.0f);
+            continue;
+        }
+        H held;
+        RowStats st = {-FLT_MAX, 0.0f, 0.0f};
+        int first = 0, n = 0;
+        for (int at = 0;;) {
+            n = min(vocab - at, H::kMost);
+            held.load(z + at, n, kMaskedBits<T>);
+            absorb_held<false>(st, held, n, heat.log2);
+            first = at;
+            if (vocab - at <= H::kMost)
+                break;
+            at += H::kMost;
+        }
+        const Teacher t = teacher_row(ta, r, vocab);
+        const bool have = t.id >= 0 && t.id < vocab;
+        const float zt = have ? load_one(z + t.id) : 0.0f;
+        st = block_stats<NT>(st, heat.log2, lds);
+        held.again();
+        const bool count = counts(t, w);
+        if (threadIdx.x < 64) {
+            const float l = row_loss(t, zt, have, w, st, heat);
+            if (threadIdx.x == 0) {
+                loss[r] = count ? l : 0.0f;
+                if (stats) {
+                    stats[2 * r] = st.m;
+                    stats[2 * r + 1] = st.s;
+                }
+            }
+        }
+        if (GRADIENT) {
+            if (!count) {
+                write_all<O, NT>(o, vocab, 0.0f);
+            } else {
+                const Gradient g = distill_gradient(t, w, st, heat);
+                write_gradient<false>(held, o + first, n, g, heat.log2);
+                for (int at = first - H::kMost; at >= 0; at -= H::kMost) {
+                    held.load(z + at, H::kMost, kMaskedBits<T>);
+                    write_gradient<false>(held, o + at, H::kMost, g, heat.log2);
+                }
+                __syncthreads();
+                if (threadIdx.x < 64 && !t.bad)
+                    write_ids(o, t, zt, 0, vocab, g, w * heat.t, ta.top_k, heat.log2);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---- gradients of chunks --------------------------------------------------------------
+
+// A chunk of a row per workgroup: short enough that a few rows fill the chip, and
+// that several workgroups share a CU, so that one's loads run under another's
+// stores.
+constexpr int kChunkNT = 256, kChunkNV = 4;
+template <class T> constexpr int kChunk = kChunkNT * kChunkNV * kElems<T>;
+
+template <class T, class O>
+__global__ void __launch_bounds__(kChunkNT)
+k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,
+                 TeacherArgs ta, const float *stats, O *dlogits, int64_t ld_o)
+{
+    using H = Held<T, kChunkNT, kChunkNV>;
+    for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
+        const int64_t r = b / chunks;
+        const int at = (int)(b - r * chunks) * H::kMost, n = min(vocab - at, H::kMost);
+        const T *z = logits + r * ld;
+        O *o = dlogits + r * ld_o;
+        const float w = ta.weight ? ta.weight[r] : 1.0f;
+        if (w == 0.0f) {
+            write_all<O, kChunkNT>(o + at, n, 0.0f);
+            continue;
+        }
+        H held;
+        held.load(z + at, n, kMaskedBits<T>);
+        const RowStats st = {stats[2 * r], stats[2 * r + 1], 0.0f};
+        const Teacher t = teacher_row(ta, r, vocab);
+        const bool mine = t.id >= at && t.id < at + n;
+        const float zt = mine ? load_one(z + t.id) : 0.0f;
+        if (!counts(t, w)) {
+            write_all<O, kChunkNT>(o + at, n, 0.0f);
+            continue;
+        }
+        // every id's logit is read before anything is written over it
+        __syncthreads();
+        const Gradient g = distill_gradient(t, w, st, heat);
+        write_gradient<false>(held, o + at, n, g, heat.log2);
+        __syncthreads();
+        if (threadIdx.x < 64 && !t.bad && __any(mine))
+            write_ids(o, t, zt, at, at + n, g, w * heat.t, ta.top_k, heat.log2);
+    }
+}
+
+template <class T, class O>
+__global__ void __launch_bounds__(kChunkNT)
+k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,
+               const int32_t *tokens, const float *stats, const float *entropy,
+               const float *d_logprob, const float *d_entropy, O *dlogits, int64_t ld_o)
+{
+    using H = Held<T, kChunkNT, kChunkNV>;
+    constexpr float kLn2 = 0.69314718055994531f;
+    for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
+        const int64_t r = b / chunks;
+        const int at = (int)(b - r * chunks) * H::kMost, n = min(vocab - at, H::kMost);
+        const T *z = logits + r * ld;
+        O *o = dlogits + r * ld_o + at;
+        H held;
+        held.load(z + at, n, kMaskedBits<T>);
+        const int token = d_logprob ? tokens[r] : -1;
+        const float gl = token < 0 ? 0.0f : token >= vocab ? NAN : d_logprob[r] * heat.inv;
+        const float gh = d_entropy ? d_entropy[r] * heat.inv : 0.0f;
+        const float m = stats[2 * r], s = stats[2 * r + 1];
+        // -(gl + gh (log q + H)) / S with log q = d - log S: a constant and a slope in d
+        Gradient g = {base_of(m), 0.0f, 0.0f};
+        if (s != 0.0f) {
+            const float c = d_entropy ? fmaf(gh, entropy[r] - logf(s), gl) : gl;
+            g.k0 = -c / s;
+            g.k1 = -gh * kLn2 / s;
+        } else if (token >= vocab) {
+            g.k0 = NAN;
+        }
+        const bool here = token >= at && token < at + n;
+        const float zt = here ? load_one(z + token) : 0.0f;
+        __syncthreads();
+        write_gradient<true>(held, o, n, g, heat.log2);
+        __syncthreads();
+        if (here && threadIdx.x == 0)
+            o[token - at] = (O)(gl + gradient_at<true>(zt, g, heat.log2));
+    }
+}
+
+mxq_status check_teacher(int64_t rows, const TeacherArgs &t)
+{
+    if (t.top_k < 1 || t.top_k > MXQ_TOP_MAX || (t.renormalize != 0 && t.renormalize != 1))
+        return MXQ_ERR_UNSUPPORTED;
+    if (rows > 0 && (!t.ids || !t.lps))
+        return MXQ_ERR_NULL;
+    return aligned4(t.ids) && aligned4(t.lps) && aligned4(t.weight) ? MXQ_OK : MXQ_ERR_ALIGN;
+}
+
+template <bool GRADIENT>
+mxq_status launch_rows(const void *logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                       const Heat &heat, const TeacherArgs &ta, float *loss, float *stats,
+                       void *dlogits, int32_t o_dtype, int64_t ld_o, hipStream_t s)
+{
+    with_type(dtype, [&](auto *tt) {
+        with_type(o_dtype, [&](auto *ot) {
+            using T = std::remove_pointer_t<decltype(tt)>;
+            using O = std::remove_pointer_t<decltype(ot)>;
+            with_threads<T>(vocab, [&](auto nt) {
+                constexpr int NT = decltype(nt)::value;
+                hipLaunchKernelGGL((k_distill_rows<T, O, NT, GRADIENT>), dim3(row_grid(rows)),
+                                   dim3(NT), 0, s, static_cast<const T *>(logits), ld, rows,
+                                   (int)vocab, heat, ta, loss, stats, static_cast<O *>(dlogits),
+                                   ld_o);
+            });
+        });
+    });
+    return launched();
+}
+
+// the chunks of a row, and the grid of a launch over them
+template <class T> int chunks_of(int64_t vocab) { return (int)((vocab + kChunk<T> - 1) / kChunk<T>); }
+unsigned chunk_grid(int64_t rows, int chunks)
+{
+    return (unsigned)(rows < kMaxGrid / chunks ? rows * chunks : kMaxGrid);
+}
+
+}  // namespace
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" mxq_status mxq_token_logprobs_backward(
+    const void *logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab, float temperature,
+    const int32_t *tokens, const float *stats, const float *entropy, const float *d_logprob,
+    const float *d_entropy, void *dlogits, int32_t dlogits_dtype, int64_t ld_dlogits, void *stream)
+{
+    mxq_status st = check_logits(logits, dtype, ld, rows, vocab, temperature);
+    if (!st)
+        st = check_gradient(dlogits, dlogits_dtype, ld_dlogits, rows, vocab);
+    if (st || rows == 0)
+        return st;
+    if (!stats || (d_logprob && !tokens) || (d_entropy && !entropy))
+        return MXQ_ERR_NULL;
+    if (!aligned4(tokens) || !aligned4(stats) || !aligned4(entropy) || !aligned4(d_logprob) ||
+        !aligned4(d_entropy))
+        return MXQ_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    with_type(dtype, [&](auto *tt) {
+        with_type(dlogits_dtype, [&](auto *ot) {
+            using T = std::remove_pointer_t<decltype(tt)>;
+            using O = std::remove_pointer_t<decltype(ot)>;
+            const int chunks = chunks_of<T>(vocab);
+            hipLaunchKernelGGL((k_logprobs_bwd<T, O>), dim3(chunk_grid(rows, chunks)),
+                               dim3(kChunkNT), 0, s, static_cast<const T *>(logits), ld, rows,
+                               (int)vocab, chunks, heat_of(temperature), tokens, stats, entropy,
+                               d_logprob, d_entropy, static_cast<O *>(dlogits), ld_dlogits);
+        });
+    });
+    return launched();
+}
+
+extern "C" mxq_status mxq_distill_forward(const void *logits, int32_t dtype, int64_t ld,
+                                          int64_t rows, int64_t vocab, float temperature,
+                                          const int32_t *teacher_ids,
+                                          const float *teacher_logprobs, int32_t top_k,
+                                          int32_t renormalize, const float *weight, float *loss,
+                                          float *stats, void *workspace, size_t ws_bytes,
+                                          void *stream)
+{
+    const TeacherArgs ta = {teacher_ids, teacher_logprobs, top_k, renormalize, weight};
+    mxq_status st = check_logits(logits, dtype, ld, rows, vocab, temperature);
+    if (!st)
+        st = check_teacher(rows, ta);
+    if (st || rows == 0)
+        return st;
+    if (!loss || !stats)
+        return MXQ_ERR_NULL;
+    if (!aligned4(loss) || !aligned4(stats) || reinterpret_cast<uintptr_t>(workspace) % 8)
+        return MXQ_ERR_ALIGN;
+    const size_t need = mxq_vocab_workspace_size(rows, vocab, 0);
+    if (need > 0 && (!workspace || ws_bytes < need))
+        return MXQ_ERR_WORKSPACE;
+    return launch_rows<false>(logits, dtype, ld, rows, vocab, heat_of(temperature), ta, loss,
+                              stats, nullptr, MXQ_OUT_F32, 0, static_cast<hipStream_t>(stream));
+}
+
+extern "C" mxq_status mxq_distill_backward(const void *logits, int32_t dtype, int64_t ld,
+                                           int64_t rows, int64_t vocab, float temperature,
+                                           const int32_t *teacher_ids,
+                                           const float *teacher_logprobs, int32_t top_k,
+                                           int32_t renormalize, const float *weight,
+                                           const float *stats, void *dlogits,
+                                           int32_t dlogits_dtype, int64_t ld_dlogits, void *stream)
+{
+    const TeacherArgs ta = {teacher_ids, teacher_logprobs, top_k, renormalize, weight};
+    mxq_status st = check_logits(logits, dtype, ld, rows, vocab, temperature);
+    if (!st)
+        st = check_gradient(dlogits, dlogits_dtype, ld_dlogits, rows, vocab);
+    if (!st)
+        st = check_teacher(rows, ta);
+    if (st || rows == 0)
+        return st;
+    if (!stats)
+        return MXQ_ERR_NULL;
+    if (!aligned4(stats))
+        return MXQ_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    with_type(dtype, [&](auto *tt) {
+        with_type(dlogits_dtype, [&](auto *ot) {
+            using T = std::remove_pointer_t<decltype(tt)>;
+            using O = std::remove_pointer_t<decltype(ot)>;
+            const int chunks = chunks_of<T>(vocab);
+            hipLaunchKernelGGL((k_distill_chunks<T, O>), dim3(chunk_grid(rows, chunks)),
+                               dim3(kChunkNT), 0, s, static_cast<const T *>(logits), ld, rows,
+                               (int)vocab, chunks, heat_of(temperature), ta, stats,
+                               static_cast<O *>(dlogits), ld_dlogits);
+        });
+    });
+    return launched();
+}
+
+extern "C" mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t rows,
+                                  int64_t vocab, float temperature, const int32_t *teacher_ids,
+                                  const float *teacher_logprobs, int32_t top_k,
+                                  int32_t renormalize, const float *weight, float *loss,
+                                  void *dlogits, int32_t dlogits_dtype, int64_t ld_dlogits,
+                                  void *workspace, size_t ws_bytes, void *stream)
+{
+    const TeacherArgs ta = {teacher_ids, teacher_logprobs, top_k, renormalize, weight};
+    mxq_status st = check_logits(logits, dtype, ld, rows, vocab, temperature);
+    if (!st)
+        st = check_gradient(dlogits, dlogits_dtype, ld_dlogits, rows, vocab);
+    if (!st)
+        st = check_teacher(rows, ta);
+    if (st || rows == 0)
+        return st;
+    if (!loss)
+        return MXQ_ERR_NULL;
+    if (!aligned4(loss) || reinterpret_cast<uintptr_t>(workspace) % 8)
+        return MXQ_ERR_ALIGN;
+    const size_t need = mxq_vocab_workspace_size(rows, vocab, 0);
+    if (need > 0 && (!workspace || ws_bytes < need))
+        return MXQ_ERR_WORKSPACE;
+    return launch_rows<true>(logits, dtype, ld, rows, vocab, heat_of(temperature), ta, loss,
+                             nullptr, dlogits, dlogits_dtype, ld_dlogits,
+                             static_cast<hipStream_t>(stream));
+}

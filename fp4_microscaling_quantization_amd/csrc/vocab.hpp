@@ -1,0 +1,205 @@
+// What the operators over a vocabulary share (token log probabilities,
+// distillation): the softmax statistics of a row, and the host's checks.
+#pragma once
+
+#include <float.h>
+
+#include "mxq_host.hpp"
+#include "rows.hpp"
+
+namespace mxq {
+
+// Vectors of 16 bytes that a thread holds of a row.  With the widest workgroup
+// (1024 threads) that is 256 KB, half of a CU's registers: 131072 bf16 or 65536
+// fp32 logits.  Longer rows take several stretches.
+constexpr int kHeld = 16;
+
+template <class T> constexpr uint32_t kMaskedBits = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+
+// What the kernels take of the temperature: 1 / T and log2(e) / T.
+struct Heat {
+    float t, inv, log2;
+};
+
+// (z - m) / T for a row's maximum m; m of a row with every logit masked counts
+// as 0, so that the differences are -inf and not NaN.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Softmax statistics: the maximum m, s = sum exp(d), a = sum exp(d) d with
+// d = (z - m) / T in units of log2 (2^d = exp).  One pass: a thread's m starts
+// at the lowest finite value, and s and a move to a new maximum as it comes.
+// The difference is taken before the product with log2(e) / T: the product of
+// the lowest finite value would be -inf, a row of such values has to be uniform.
+struct RowStats {
+    float m, s, a;
+};
+constexpr float kFloorLog2 = -256.0f;  // 2^d is 0 far above it: d stays finite in a
+
+// s and a of a state, seen from a maximum `to` >= its own.  Far below it (2^-256
+// is 0 in fp32) they are 0; NaN stays NaN.
+__device__ __forceinline__ void move_to(RowStats &st, float to, float log2)
+{
+    const float d = fmaxf((st.m - to) * log2, kFloorLog2);
+    const float e = __builtin_amdgcn_exp2f(d);
+    st.a = e * fmaf(st.s, d, st.a);
+    st.s *= e;
+    st.m = to;
+}
+
+template <bool ENTROPY, int N>
+__device__ __forceinline__ void absorb(RowStats &st, const float (&f)[N], float log2)
+{
+    float m = f[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j)
+        m = fmaxf(m, f[j]);
+    m = fmaxf(st.m, m);
+    const float d = fmaxf((st.m - m) * log2, kFloorLog2);
+    const float sc = __builtin_amdgcn_exp2f(d);
+    if (ENTROPY)
+        st.a = sc * fmaf(st.s, d, st.a);
+    float s = 0.0f, a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float dj = (f[j] - m) * log2;
+        const float e = __builtin_amdgcn_exp2f(dj);
+        s += e;
+        if (ENTROPY)
+            a = fmaf(e, fmaxf(dj, kFloorLog2), a);
+    }
+    st.s = fmaf(st.s, sc, s);
+    if (ENTROPY)
+        st.a += a;
+    st.m = m;
+}
+
+// The statistics of n elements at p, into the threads' own states; the held
+// vectors stay in h.  16 elements at a time: what a step costs beside its
+// exponentials is shared by them.
+template <bool ENTROPY, class T, int NT>
+__device__ __forceinline__ void absorb_held(RowStats &st, const Held<T, NT, kHeld> &h, int n,
+                                            float log2)
+{
+    constexpr int E = kElems<T>, G = 16 / E;
+#pragma unroll
+    for (int i = 0; i < kHeld; i += G) {
+        if (h.any(i, n)) {
+            float f[16];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float part[E];
+                h.get(i + g, part);
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    f[g * E + j] = part[j];
+            }
+            absorb<ENTROPY>(st, f, log2);
+        }
+    }
+}
+
+// The workgroup's statistics from its threads', in every thread, joined in a
+// fixed order; m is -inf where s is 0.  lds: 3 NT / 64 floats.
+template <int NT>
+__device__ __forceinline__ RowStats block_stats(RowStats st, float log2, float *lds)
+{
+    constexpr int W = NT / 64;
+    move_to(st, wave_max(st.m), log2);
+    st.s = wave_sum(st.s);
+    st.a = wave_sum(st.a);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+        const int w = threadIdx.x >> 6;
+        lds[w] = st.m;
+        lds[W + w] = st.s;
+        lds[2 * W + w] = st.a;
+    }
+    __syncthreads();
+    float m = lds[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w)
+        m = fmaxf(m, lds[w]);
+    RowStats all = {m, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        RowStats one = {lds[w], lds[W + w], lds[2 * W + w]};
+        move_to(one, m, log2);
+        all.s += one.s;
+        all.a += one.a;
+    }
+    if (all.s == 0.0f)
+        all.m = -INFINITY;
+    return all;
+}
+
+// log q of a logit; -inf throughout a row with every logit masked
+__device__ __forceinline__ float log_q(float z, const RowStats &st, const Heat &h)
+{
+    return st.s == 0.0f ? -INFINITY : (z - base_of(st.m)) * h.inv - logf(st.s);
+}
+
+// ---- the host's side -------------------------------------------------------------
+
+constexpr int64_t kMaxGrid = 1 << 20;  // workgroups of a launch over rows; more rows loop
+
+inline unsigned row_grid(int64_t rows) { return (unsigned)(rows < kMaxGrid ? rows : kMaxGrid); }
+inline Heat heat_of(float t)
+{
+    return {t, (float)(1.0 / (double)t), (float)(1.4426950408889634 / (double)t)};
+}
+inline bool dtype_ok(int32_t d) { return d == MXQ_OUT_F32 || d == MXQ_OUT_BF16; }
+inline bool aligned(const void *p, int32_t d)
+{
+    return reinterpret_cast<uintptr_t>(p) % (d == MXQ_OUT_F32 ? 4 : 2) == 0;
+}
+inline bool aligned4(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+inline mxq_status launched() { return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_DEVICE; }
+
+// f(null pointer of the element type) for a dtype code that was checked
+template <class F> void with_type(int32_t d, F f)
+{
+    if (d == MXQ_OUT_F32)
+        f((float *)nullptr);
+    else
+        f((bf16_t *)nullptr);
+}
+
+// f(integral constant: threads of a workgroup) for a row of n elements of T: the
+// fewest that hold it, so that short rows share a CU, and the widest beyond.
+template <class T, class F> void with_threads(int64_t n, F f)
+{
+    constexpr int64_t one = 64 * kHeld * kElems<T>;  // what a wave holds
+    if (n <= 4 * one)
+        f(std::integral_constant<int, 256>());
+    else if (n <= 8 * one)
+        f(std::integral_constant<int, 512>());
+    else
+        f(std::integral_constant<int, 1024>());
+}
+
+// The checks that every call over a vocabulary shares: the logits and the
+// temperature (1 / temperature has to be finite).
+inline mxq_status check_logits(const void *logits, int32_t dtype, int64_t ld, int64_t rows,
+                               int64_t vocab, float temperature)
+{
+    if (!dtype_ok(dtype) || !(temperature >= FLT_MIN) || !(temperature < INFINITY))
+        return MXQ_ERR_UNSUPPORTED;
+    if (rows < 0 || vocab < 1 || vocab > INT32_MAX || ld < vocab)
+        return MXQ_ERR_SHAPE;
+    if (rows > 0 && !logits)
+        return MXQ_ERR_NULL;
+    return aligned(logits, dtype) ? MXQ_OK : MXQ_ERR_ALIGN;
+}
+inline mxq_status check_gradient(const void *dlogits, int32_t dtype, int64_t ld, int64_t rows,
+                                 int64_t vocab)
+{
+    if (!dtype_ok(dtype))
+        return MXQ_ERR_UNSUPPORTED;
+    if (ld < vocab)
+        return MXQ_ERR_SHAPE;
+    if (rows > 0 && !dlogits)
+        return MXQ_ERR_NULL;
+    return aligned(dlogits, dtype) ? MXQ_OK : MXQ_ERR_ALIGN;
+}
+
+}  // namespace mxq

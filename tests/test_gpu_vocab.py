@@ -115,6 +115,22 @@ def test_top_clustered(mxq_lib, vocab, rows):
             assert torch.equal(out[3].cpu().long(), ids.expand(rows, 64)), (vocab, step, dtype)
 
 
+@pytest.mark.parametrize("vocab", [20000, 131072, 300007])
+def test_top_stretches(mxq_lib, vocab):
+    """Long stretches of large logits, one every few thousand entries: a few
+    threads hold far more of them than are asked for; and rows of equal ones."""
+    for step, width in ((2048, 128), (4096, 300), (8192, 128), (8192, 1000), (16384, 4096)):
+        for dtype in (F32, BF16):
+            for equal in (False, True):
+                say("stretches", vocab, step, width, dtype, equal)
+                z = rand((2, vocab), step, F32, 0.5)
+                at = torch.arange(vocab) % step < width
+                z[:, at] = 20.0 if equal else 20.0 + 4 * rand((2, int(at.sum())), 9)
+                z = z.to(dtype)
+                out = mxq_lib.token_logprobs(z.to(dev()), top_k=64)
+                assert torch.equal(out[3].cpu().long(), ref.Distribution(z, 1.0).top(64)), (vocab, step, dtype)
+
+
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 def test_logprobs_backward(mxq_lib, shape):
     m = mxq_lib
