@@ -88,6 +88,7 @@ __device__ __forceinline__ void write_gradient(const Held<T, NT, NV> &held, O *o
                                                const Gradient &g, float log2)
 {
     constexpr int E = kElems<T>;
+    n = fresh(n);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (held.any(i, n)) {
@@ -165,7 +166,7 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
         int first = 0, n = 0;
         for (int at = 0;;) {
             n = min(vocab - at, H::kMost);
-            held.load(z + at, n, kMaskedBits<T>);
+            held.load(z + at, fresh(n), kMaskedBits<T>);
             absorb_held<false>(st, held, n, heat.log2);
             first = at;
             if (vocab - at <= H::kMost)

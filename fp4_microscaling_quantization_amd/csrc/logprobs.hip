@@ -134,10 +134,11 @@ __device__ __forceinline__ uint64_t top_held(uint64_t best, Held<T, NT, kHeld> &
         asm volatile("" : "+v"(mine));
         __syncthreads();
         const float least = key_value(bound);
+        const int n2 = fresh(n);
         if (__any(most >= least)) {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-                if (!held.any(i, n))
+                if (!held.any(i, n2))
                     continue;
                 float f[E];
                 held.get(i, f);
@@ -228,7 +229,7 @@ k_logprobs(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, Logp
         uint64_t list = 0;
         for (int at = 0;;) {
             const int n = min(vocab - at, H::kMost);
-            held.load(z + at, n, kMaskedBits<T>);
+            held.load(z + at, fresh(n), kMaskedBits<T>);
             absorb_held<true>(st, held, n, heat.log2);
             if (TOP)
                 list = top_held(list, held, at, n, st.m, out.top_k, keys, buffer, &count);

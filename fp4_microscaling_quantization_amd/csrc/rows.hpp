@@ -114,6 +114,15 @@ template <class T> __device__ __forceinline__ gv4u load_some(const T *p, int lef
     return v;
 }
 
+// A uniform value that the compiler takes for a new one: what a pass derives from it
+// (the predicates of a row's last, partial vectors) is made again in the next pass
+// and not kept in registers for it.
+__device__ __forceinline__ int fresh(int v)
+{
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
 // The thread's vector of the NT vectors of E elements at p: a uniform address and
 // an unsigned offset, so that no 64-bit address per vector is kept in registers.
 template <int E, class T> __device__ __forceinline__ T *lane_at(T *p)
