@@ -97,9 +97,8 @@ __device__ __forceinline__ void write_gradient(const Held<T, NT, NV> &held, O *o
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 f[j] = gradient_at<SLOPE>(f[j], g, log2);
-            store_held<O, NT>(o, i, n, f);
+            held.put(o, i, n, f);
         }
-        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -111,8 +110,14 @@ template <class O, int NT> __device__ __forceinline__ void write_all(O *o, int n
 #pragma unroll
     for (int j = 0; j < E; ++j)
         f[j] = value;
-    for (int64_t at = (int)threadIdx.x * E; at < n; at += NT * E)
-        store_some(o + at, f, (int)(n - at));
+    for (int64_t at = (int)threadIdx.x * E; at < n; at += NT * E) {
+        if (at + E <= n) {
+            store_vec(o + at, f);
+        } else {
+            for (int64_t k = at; k < n; ++k)
+                o[k] = (O)value;
+        }
+    }
 }
 
 // The entries of the teacher's ids in [from, to) once more, with their p: zt is the
@@ -138,7 +143,7 @@ __device__ __forceinline__ void write_ids(O *o, const Teacher &t, float zt, int 
 // One workgroup per row: loss (stats where asked for), and with GRADIENT dlogits.
 // Rows longer than the registers hold: the stretches before the last are read
 // again for the gradient, from the last-level cache, where one row per CU stays.
-template <class T, class O, int NT, bool GRADIENT>
+template <class T, class O, int NT, bool GRADIENT, bool SHORT>
 __global__ void __launch_bounds__(NT, 4)
 k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, TeacherArgs ta,
                float *loss, float *stats, O *dlogits, int64_t ld_o)
@@ -166,8 +171,9 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
         int first = 0, n = 0;
         for (int at = 0;;) {
             n = min(vocab - at, H::kMost);
-            held.load(z + at, fresh(n), kMaskedBits<T>);
-            absorb_held<false>(st, held, n, heat.log2);
+            held.template load<SHORT>(z + at, n);
+            float most[kGroups<T>];
+            absorb_held<false>(st, held, n, heat.log2, most);
             first = at;
             if (vocab - at <= H::kMost)
                 break;
@@ -196,7 +202,7 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
                 const Gradient g = distill_gradient(t, w, st, heat);
                 write_gradient<false>(held, o + first, n, g, heat.log2);
                 for (int at = first - H::kMost; at >= 0; at -= H::kMost) {
-                    held.load(z + at, H::kMost, kMaskedBits<T>);
+                    held.template load<SHORT>(z + at, H::kMost);
                     write_gradient<false>(held, o + at, H::kMost, g, heat.log2);
                 }
                 __syncthreads();
@@ -216,7 +222,7 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
 constexpr int kChunkNT = 256, kChunkNV = 4;
 template <class T> constexpr int kChunk = kChunkNT * kChunkNV * kElems<T>;
 
-template <class T, class O>
+template <class T, class O, bool SHORT>
 __global__ void __launch_bounds__(kChunkNT)
 k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,
                  TeacherArgs ta, const float *stats, O *dlogits, int64_t ld_o)
@@ -233,7 +239,7 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
             continue;
         }
         H held;
-        held.load(z + at, n, kMaskedBits<T>);
+        held.template load<SHORT>(z + at, n);
         const RowStats st = {stats[2 * r], stats[2 * r + 1], 0.0f};
         const Teacher t = teacher_row(ta, r, vocab);
         const bool mine = t.id >= at && t.id < at + n;
@@ -242,7 +248,8 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
             write_all<O, kChunkNT>(o + at, n, 0.0f);
             continue;
         }
-        // every id's logit is read before anything is written over it
+        // everything is read before anything is written over it
+        held.again();
         __syncthreads();
         const Gradient g = distill_gradient(t, w, st, heat);
         write_gradient<false>(held, o + at, n, g, heat.log2);
@@ -252,7 +259,7 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
     }
 }
 
-template <class T, class O>
+template <class T, class O, bool SHORT>
 __global__ void __launch_bounds__(kChunkNT)
 k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,
                const int32_t *tokens, const float *stats, const float *entropy,
@@ -266,7 +273,7 @@ k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks,
         const T *z = logits + r * ld;
         O *o = dlogits + r * ld_o + at;
         H held;
-        held.load(z + at, n, kMaskedBits<T>);
+        held.template load<SHORT>(z + at, n);
         const int token = d_logprob ? tokens[r] : -1;
         const float gl = token < 0 ? 0.0f : token >= vocab ? NAN : d_logprob[r] * heat.inv;
         const float gh = d_entropy ? d_entropy[r] * heat.inv : 0.0f;
@@ -282,6 +289,7 @@ k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks,
         }
         const bool here = token >= at && token < at + n;
         const float zt = here ? load_one(z + token) : 0.0f;
+        held.again();
         __syncthreads();
         write_gradient<true>(held, o, n, g, heat.log2);
         __syncthreads();
@@ -308,9 +316,10 @@ mxq_status launch_rows(const void *logits, int32_t dtype, int64_t ld, int64_t ro
         with_type(o_dtype, [&](auto *ot) {
             using T = std::remove_pointer_t<decltype(tt)>;
             using O = std::remove_pointer_t<decltype(ot)>;
-            with_threads<T>(vocab, [&](auto nt) {
+            with_threads<T>(vocab, [&](auto nt, auto is_short) {
                 constexpr int NT = decltype(nt)::value;
-                hipLaunchKernelGGL((k_distill_rows<T, O, NT, GRADIENT>), dim3(row_grid(rows)),
+                constexpr bool SHORT = decltype(is_short)::value;
+                hipLaunchKernelGGL((k_distill_rows<T, O, NT, GRADIENT, SHORT>), dim3(row_grid(rows)),
                                    dim3(NT), 0, s, static_cast<const T *>(logits), ld, rows,
                                    (int)vocab, heat, ta, loss, stats, static_cast<O *>(dlogits),
                                    ld_o);
@@ -354,10 +363,11 @@ extern "C" mxq_status mxq_token_logprobs_backward(
             using T = std::remove_pointer_t<decltype(tt)>;
             using O = std::remove_pointer_t<decltype(ot)>;
             const int chunks = chunks_of<T>(vocab);
-            hipLaunchKernelGGL((k_logprobs_bwd<T, O>), dim3(chunk_grid(rows, chunks)),
-                               dim3(kChunkNT), 0, s, static_cast<const T *>(logits), ld, rows,
-                               (int)vocab, chunks, heat_of(temperature), tokens, stats, entropy,
-                               d_logprob, d_entropy, static_cast<O *>(dlogits), ld_dlogits);
+            const auto k = vocab < kElems<T> ? k_logprobs_bwd<T, O, true> : k_logprobs_bwd<T, O, false>;
+            hipLaunchKernelGGL(k, dim3(chunk_grid(rows, chunks)), dim3(kChunkNT), 0, s,
+                               static_cast<const T *>(logits), ld, rows, (int)vocab, chunks,
+                               heat_of(temperature), tokens, stats, entropy, d_logprob, d_entropy,
+                               static_cast<O *>(dlogits), ld_dlogits);
         });
     });
     return launched();
@@ -414,10 +424,11 @@ extern "C" mxq_status mxq_distill_backward(const void *logits, int32_t dtype, in
             using T = std::remove_pointer_t<decltype(tt)>;
             using O = std::remove_pointer_t<decltype(ot)>;
             const int chunks = chunks_of<T>(vocab);
-            hipLaunchKernelGGL((k_distill_chunks<T, O>), dim3(chunk_grid(rows, chunks)),
-                               dim3(kChunkNT), 0, s, static_cast<const T *>(logits), ld, rows,
-                               (int)vocab, chunks, heat_of(temperature), ta, stats,
-                               static_cast<O *>(dlogits), ld_dlogits);
+            const auto k = vocab < kElems<T> ? k_distill_chunks<T, O, true> : k_distill_chunks<T, O, false>;
+            hipLaunchKernelGGL(k, dim3(chunk_grid(rows, chunks)), dim3(kChunkNT), 0, s,
+                               static_cast<const T *>(logits), ld, rows, (int)vocab, chunks,
+                               heat_of(temperature), ta, stats, static_cast<O *>(dlogits),
+                               ld_dlogits);
         });
     });
     return launched();

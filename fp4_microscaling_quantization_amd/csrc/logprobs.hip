@@ -44,23 +44,33 @@ template <int X> __device__ __forceinline__ uint64_t key_xor(uint64_t k)
     }
     return ((uint64_t)hi << 32) | lo;
 }
-// one step of a bitonic network: lanes X apart, the larger key to the lower lane
-// where `falling`
+// one step of a bitonic network: lanes X apart, the larger one to the lower lane where
+// `falling`; for keys and for values
 template <int X> __device__ __forceinline__ uint64_t order_step(uint64_t k, bool falling)
 {
     const uint64_t other = key_xor<X>(k);
     const bool lower = (threadIdx.x & X) == 0;
     return (k > other) == (lower == falling) ? k : other;
 }
-template <int X> __device__ __forceinline__ uint64_t order_steps(uint64_t k, bool falling)
+template <int X> __device__ __forceinline__ uint32_t order_step(uint32_t v, bool falling)
+{
+    uint32_t other;
+    if constexpr (X < 16)
+        other = lane_xor<X>(v);
+    else
+        other = (uint32_t)__shfl_xor((int)v, X);
+    const bool lower = (threadIdx.x & X) == 0;
+    return lower == falling ? max(v, other) : min(v, other);
+}
+template <int X, class K> __device__ __forceinline__ K order_steps(K k, bool falling)
 {
     k = order_step<X>(k, falling);
     if constexpr (X > 1)
         k = order_steps<X / 2>(k, falling);
     return k;
 }
-// a wave's 64 keys in falling order
-__device__ __forceinline__ uint64_t wave_sort(uint64_t k)
+// a wave's 64 keys or values in falling order
+template <class K> __device__ __forceinline__ K wave_sort(K k)
 {
     const int lane = threadIdx.x & 63;
     k = order_steps<1>(k, (lane & 2) == 0);
@@ -70,108 +80,127 @@ __device__ __forceinline__ uint64_t wave_sort(uint64_t k)
     k = order_steps<16>(k, (lane & 32) == 0);
     return order_steps<32>(k, true);
 }
-// the first 64 of two falling lists, in falling order; the second one is given
-// turned round (lane l has its 63 - l th), so the larger of each pair are the
-// first 64 and rise and fall once
-__device__ __forceinline__ uint64_t wave_merge(uint64_t a, uint64_t b_turned)
+__device__ __forceinline__ uint64_t turned(uint64_t k)
 {
-    return order_steps<32>(a > b_turned ? a : b_turned, true);
+    return (uint64_t)__shfl((unsigned long long)k, 63 - (threadIdx.x & 63));
+}
+__device__ __forceinline__ uint32_t turned(uint32_t v)
+{
+    return (uint32_t)__shfl((int)v, 63 - (threadIdx.x & 63));
+}
+// the first 64 of two falling lists, in falling order: with one turned round, the
+// larger of each pair are the first 64, and rise and fall once
+template <class K> __device__ __forceinline__ K wave_merge(K a, K b)
+{
+    b = turned(b);
+    return order_steps<32>(a > b ? a : b, true);
 }
 
-// The first 64 of the workgroup's NT keys, in falling order, in the lanes of every
-// wave.  lds: NT keys.
-template <int NT> __device__ __forceinline__ uint64_t block_top(uint64_t k, uint64_t *lds)
-{
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    k = wave_sort(k);
-    __syncthreads();
-#pragma unroll
-    for (int half = NT / 128; half >= 1; half /= 2) {
-        if (w >= half && w < 2 * half)
-            lds[threadIdx.x] = k;
-        __syncthreads();
-        if (w < half)
-            k = wave_merge(k, lds[(w + half) * 64 + 63 - lane]);
-    }
-    if (w == 0)
-        lds[lane] = k;
-    __syncthreads();
-    return lds[lane];
-}
+// What the search for the alternatives keeps in LDS.
+constexpr int kNT = 256;
+constexpr int kBuffer = 512, kPlaces = 128;
+struct Search {
+    uint64_t buffer[kBuffer];
+    uint64_t bound;
+    uint32_t most[kPlaces];
+    int count;
+};
 
-// The first top_k alternatives of the held stretch (n logits, the first of them
-// entry `at` of the row) and of the list `best` from before it, as a list again.
-//
-// A bound that top_k alternatives reach is known at once: the top_k th of the
-// threads' maxima over the row so far (`most`; a thread without an alternative has
-// the lowest finite value, which bounds nothing).  What reaches it goes to a buffer of NT keys; random rows have
-// hardly more than top_k such entries.  Where the buffer is too small (many equal
-// logits, or the large ones all in a few threads), the top_k th of what it holds is a
-// higher bound, and the search goes again, until it is not.  Every entry of the
-// buffer is an alternative of the row, so each bound leaves top_k above it.
-template <class T, int NT>
-__device__ __forceinline__ uint64_t top_held(uint64_t best, Held<T, NT, kHeld> &held, int at, int n,
-                                             float most, int top_k, uint64_t *lds,
-                                             uint64_t *buffer, int *count)
+// the first 64 of the falling list `list` and of n keys in LDS, by one wave
+__device__ __forceinline__ uint64_t list_of(uint64_t list, const uint64_t *keys, int n)
 {
-    constexpr int E = kElems<T>;
     const int lane = threadIdx.x & 63;
-    auto kth = [&](uint64_t list) {
-        const uint64_t k = (uint64_t)__shfl((unsigned long long)list, top_k - 1);
+    for (int at = 0; at < n; at += 64) {
+        const uint64_t k = wave_sort(at + lane < n ? keys[at + lane] : (uint64_t)0);
+        list = __all(list == 0) ? k : wave_merge(list, k);
+    }
+    return list;
+}
+
+// The first top_k alternatives of the held stretch (n logits, the first of them entry
+// `at` of the row) and of wave 0's list from before it, as wave 0's list.  most: the
+// thread's maxima of its groups of 16, top: its maximum over the row so far (the lowest
+// finite value where it has none).
+//
+// A bound that top_k alternatives reach is known at once: the threads' maxima go
+// into 128 (64) places, the largest of each stays, and the top_k th of those is the
+// bound; twice as many places as alternatives keep it close (a random row has about
+// 1.4 top_k logits that reach it).  Each wave goes over its registers, the groups whose
+// maximum reaches the bound, and puts what it finds into a buffer, which wave 0
+// sorts.  Where the buffer is too small (many equal logits, or the large ones all in a
+// few threads), the top_k th of what it holds is a higher bound, and the search goes
+// again, until it is not: every key of the buffer is an alternative of the row.
+// Measured beside it (1501 x 50257 fp32, 64 alternatives, 73 us): listing the groups
+// and reading them again with all lanes, 80 us, as the reads queue behind the other
+// workgroups' streams; ordering by counting larger keys with all waves, 106 us.
+template <class T>
+__device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, kNT, kHeld> &held, int at, int n,
+                                             const float (&most)[kGroups<T>], float top, int top_k,
+                                             Search &lds)
+{
+    constexpr int E = kElems<T>, G = kGroup<T>;
+    const int lane = threadIdx.x & 63, places = top_k > 32 ? kPlaces : kPlaces / 2;
+    const auto kth = [&](uint64_t l) {
+        const uint64_t k = (uint64_t)__shfl((unsigned long long)l, top_k - 1);
         return k > kLeastKey ? k : kLeastKey;
     };
-    uint64_t bound = kth(block_top<NT>((uint64_t)order_of(most) << 32, lds));
-    const uint64_t before = kth(best);
-    bound = bound > before ? bound : before;
+    if (threadIdx.x < kPlaces)
+        lds.most[threadIdx.x] = 0;
+    __syncthreads();
+    atomicMax(&lds.most[threadIdx.x & (places - 1)], order_of(top));
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        uint32_t v = wave_sort(lds.most[lane]);
+        if (places == kPlaces)
+            v = wave_merge(v, wave_sort(lds.most[64 + lane]));
+        const uint64_t k = kth((uint64_t)v << 32), before = kth(list);
+        if (lane == 0) {
+            lds.bound = k > before ? k : before;
+            lds.count = 0;
+        }
+    }
+    __syncthreads();
     for (;;) {
-        // the list so far is in the buffer from the start
-        if (threadIdx.x < 64)
-            buffer[threadIdx.x] = best;
-        if (threadIdx.x == 0)
-            *count = 64;
+        const uint64_t bound = lds.bound;
+        const float least = key_value(bound);
         held.again();
+        const int n2 = fresh(n);
         int mine = at + held.at(0);  // opaque, or the indices of all entries are kept in registers
         asm volatile("" : "+v"(mine));
-        __syncthreads();
-        const float least = key_value(bound);
-        const int n2 = fresh(n);
-        if (__any(most >= least)) {
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                if (!held.any(i, n2))
-                    continue;
+        for (int i = 0; i < kHeld; i += G) {
+            if (!__any(most[i / G] >= least))
+                continue;
+#pragma unroll
+            for (int k = i; k < i + G; ++k) {
                 float f[E];
-                held.get(i, f);
-                float m = f[0];
-#pragma unroll
-                for (int j = 1; j < E; ++j)
-                    m = fmaxf(m, f[j]);
-                if (!__any(m >= least))
-                    continue;
+                held.get(k, n2, -INFINITY, f);
+                const int back = held.whole(k, n2) ? 0 : held.skip(k, n2);
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    const uint64_t key = key_of(f[j], mine + i * NT * E + j);
-                    const bool in = f[j] >= least && key >= bound;
-                    const uint64_t mask = __ballot(in);
-                    if (mask == 0)
-                        continue;
-                    // one atomic for the wave's lanes
-                    const int leader = __ffsll((unsigned long long)mask) - 1;
-                    int to = 0;
-                    if (lane == leader)
-                        to = atomicAdd(count, __popcll(mask));
-                    to = __shfl(to, leader) + __popcll(mask & ((1ull << lane) - 1));
-                    if (in && to < NT)
-                        buffer[to] = key;
+                    if (f[j] >= least) {
+                        const uint64_t key = key_of(f[j], mine - back + k * kNT * E + j);
+                        if (key >= bound) {
+                            const int to = atomicAdd(&lds.count, 1);
+                            if (to < kBuffer)
+                                lds.buffer[to] = key;
+                        }
+                    }
                 }
             }
         }
         __syncthreads();
-        const int have = *count;
-        const uint64_t list = block_top<NT>((int)threadIdx.x < have ? buffer[threadIdx.x] : 0, lds);
-        if (have <= NT)
-            return list;
-        bound = kth(list);
+        const int have = lds.count;
+        if (have <= kBuffer)
+            return threadIdx.x < 64 ? list_of(list, lds.buffer, have) : 0;
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            const uint64_t k = kth(list_of(list, lds.buffer, kBuffer));
+            if (lane == 0) {
+                lds.bound = k;
+                lds.count = 0;
+            }
+        }
         __syncthreads();
     }
 }
@@ -214,30 +243,30 @@ __device__ __forceinline__ void write_row(const LogprobOut &out, const T *z, int
     }
 }
 
-template <class T, int NT, bool TOP>
-__global__ void __launch_bounds__(NT, 4)
+template <class T, bool TOP, bool SHORT>
+__global__ void __launch_bounds__(kNT, 4)
 k_logprobs(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, LogprobOut out)
 {
-    using H = Held<T, NT, kHeld>;
-    __shared__ float lds[3 * NT / 64];
-    __shared__ uint64_t keys[TOP ? NT : 1], buffer[TOP ? NT : 1];
-    __shared__ int count;
+    using H = Held<T, kNT, kHeld>;
+    __shared__ float lds[3 * kNT / 64];
+    __shared__ typename std::conditional<TOP, Search, char>::type search;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *z = logits + r * ld;
-        H held;
         RowStats st = {-FLT_MAX, 0.0f, 0.0f};
         uint64_t list = 0;
         for (int at = 0;;) {
             const int n = min(vocab - at, H::kMost);
-            held.load(z + at, fresh(n), kMaskedBits<T>);
-            absorb_held<true>(st, held, n, heat.log2);
-            if (TOP)
-                list = top_held(list, held, at, n, st.m, out.top_k, keys, buffer, &count);
+            H held;
+            held.template load<SHORT>(z + at, n);
+            float most[kGroups<T>];
+            absorb_held<true>(st, held, n, heat.log2, most);
+            if constexpr (TOP)
+                list = top_held(list, held, at, n, most, st.m, out.top_k, search);
             if (vocab - at <= H::kMost)
                 break;
             at += H::kMost;
         }
-        st = block_stats<NT>(st, heat.log2, lds);
+        st = block_stats<kNT>(st, heat.log2, lds);
         if (threadIdx.x < 64)
             write_row(out, z, r, vocab, st, list, heat);
         __syncthreads();
@@ -285,16 +314,12 @@ extern "C" mxq_status mxq_token_logprobs(const void *logits, int32_t dtype, int6
     hipStream_t s = static_cast<hipStream_t>(stream);
     with_type(dtype, [&](auto *tt) {
         using T = std::remove_pointer_t<decltype(tt)>;
-        with_threads<T>(vocab, [&](auto nt) {
-            constexpr int NT = decltype(nt)::value;
-            const auto *z = static_cast<const T *>(logits);
-            if (top_k > 0)
-                hipLaunchKernelGGL((k_logprobs<T, NT, true>), dim3(row_grid(rows)), dim3(NT), 0, s,
-                                   z, ld, rows, (int)vocab, heat_of(temperature), out);
-            else
-                hipLaunchKernelGGL((k_logprobs<T, NT, false>), dim3(row_grid(rows)), dim3(NT), 0,
-                                   s, z, ld, rows, (int)vocab, heat_of(temperature), out);
-        });
+        const bool is_short = vocab < kElems<T>;
+        const auto k = top_k > 0 ? (is_short ? k_logprobs<T, true, true> : k_logprobs<T, true, false>)
+                                 : (is_short ? k_logprobs<T, false, true> : k_logprobs<T, false, false>);
+        hipLaunchKernelGGL(k, dim3(row_grid(rows)), dim3(kNT), 0, s,
+                           static_cast<const T *>(logits), ld, rows, (int)vocab,
+                           heat_of(temperature), out);
     });
     return launched();
 }

@@ -25,23 +25,28 @@ struct FwdArgs {
     float *mean, *rstd;
 };
 
-// n gamma + beta of the E columns from c on, of which `left` are there (WHOLE: all)
-template <bool WHOLE, int E>
-__device__ __forceinline__ void affine(float (&f)[E], const FwdArgs &a, int c, int left)
+// n gamma + beta of the E columns from c on; rows shorter than a vector start at a
+// negative c
+template <bool SHORT, int E>
+__device__ __forceinline__ void affine(float (&f)[E], const FwdArgs &a, int c)
 {
-    const auto columns = [&](const float *p, int j) {
-        return WHOLE ? load_vec(p + c + j) : load_some(p + c + j, left - j, 0u);
-    };
+    if (SHORT) {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            if (c + j >= 0)
+                f[j] = f[j] * (a.gamma ? a.gamma[c + j] : 1.0f) + (a.beta ? a.beta[c + j] : 0.0f);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < E; j += 4) {
         if (a.gamma) {
-            const gv4u v = columns(a.gamma, j);
+            const gv4u v = load_vec(a.gamma + c + j);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 f[j + k] *= as_f(v[k]);
         }
         if (a.beta) {
-            const gv4u v = columns(a.beta, j);
+            const gv4u v = load_vec(a.beta + c + j);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 f[j + k] += as_f(v[k]);
@@ -61,21 +66,19 @@ template <int NT> __device__ __forceinline__ float row_sum(float v, float *lds)
 // is read again for each of the three passes.  The variance is the mean square of
 // the differences from the mean, a second pass over registers: mean(x^2) - mu^2
 // loses what the two have in common.
-template <class X, int NT, int NV, bool LONG>
+template <class X, int NT, int NV, bool LONG, bool SHORT>
 __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
 {
     using H = Held<X, NT, NV>;
     constexpr int E = kElems<X>;
-    using Whole = std::integral_constant<bool, true>;
-    using Part = std::integral_constant<bool, false>;
     __shared__ float lds[NT / 64];
     const float inv = 1.0f / (float)a.cols;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const X *xr = x + r * a.ld_x;
         H h;
         if (!LONG)
-            h.load(xr, fresh(a.cols), 0u);
-        // f(vector, its first column, how many are there, whether all of every thread's are)
+            h.template load<SHORT>(xr, a.cols);
+        // f(vector's number, the stretch's first column, its columns)
         const auto each = [&](auto f) {
             const int cols = fresh(a.cols);
             if (!LONG)
@@ -83,17 +86,12 @@ __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
             for (int at = 0;;) {
                 const int n = min(cols - at, H::kMost);
                 if (LONG)
-                    h.load(xr + at, n, 0u);
+                    h.template load<SHORT>(xr + at, n);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     if (!h.any(i, n))
                         break;
-                    float v[E];
-                    h.get(i, v);
-                    if ((i + 1) * NT * E <= n)
-                        f(v, at + h.at(i), E, Whole());
-                    else
-                        f(v, at + h.at(i), n - h.at(i), Part());
+                    f(i, at, n);
                 }
                 if (!LONG || cols - at <= H::kMost)
                     break;
@@ -103,7 +101,9 @@ __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
         float mu = 0.0f;
         if (a.layer) {
             float s = 0.0f;
-            each([&](const float (&v)[E], int, int, auto) {
+            each([&](int i, int, int n) {
+                float v[E];
+                h.get(i, n, 0.0f, v);
 #pragma unroll
                 for (int j = 0; j < E; ++j)
                     s += v[j];
@@ -111,26 +111,25 @@ __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
             mu = row_sum<NT>(s, lds) * inv;
         }
         float s2 = 0.0f;
-        each([&](const float (&v)[E], int, int left, auto whole) {
+        each([&](int i, int, int n) {
+            float v[E];
+            h.get(i, n, mu, v);
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const float d = whole || j < left ? v[j] - mu : 0.0f;
-                s2 = fmaf(d, d, s2);
-            }
+            for (int j = 0; j < E; ++j)
+                s2 = fmaf(v[j] - mu, v[j] - mu, s2);
         });
         const float rs = 1.0f / sqrtf(row_sum<NT>(s2, lds) * inv + a.eps);
-        each([&](float (&v)[E], int c, int left, auto whole) {
+        each([&](int i, int at, int n) {
+            float v[E];
+            h.get(i, v);
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 v[j] = (v[j] - mu) * rs;
-            affine<whole>(v, a, c, left);
-            if (a.y_dtype == MXQ_OUT_F32) {
-                float *y = (float *)a.y + r * a.ld_y + c;
-                whole ? store_vec(y, v) : store_some(y, v, left);
-            } else {
-                bf16_t *y = (bf16_t *)a.y + r * a.ld_y + c;
-                whole ? store_vec(y, v) : store_some(y, v, left);
-            }
+            affine<SHORT>(v, a, at + h.start(i, n));
+            if (a.y_dtype == MXQ_OUT_F32)
+                h.put((float *)a.y + r * a.ld_y + at, i, n, v);
+            else
+                h.put((bf16_t *)a.y + r * a.ld_y + at, i, n, v);
         });
         if (threadIdx.x == 0) {
             if (a.mean && a.layer)
@@ -157,12 +156,11 @@ struct BwdArgs {
 template <class T> struct Unit {
     static constexpr int V = 8 / kElems<T>;
     gv4u v[V];
-    __device__ __forceinline__ void load(const T *p, int left)
+    __device__ __forceinline__ void load(const T *p)
     {
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            v[k] = left >= 8 ? load_vec(p + k * kElems<T>)
-                             : load_some(p + k * kElems<T>, left - k * kElems<T>, 0u);
+            v[k] = load_vec(p + k * kElems<T>);
     }
     // as Held::again
     __device__ __forceinline__ void again()
@@ -202,8 +200,8 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
     float gamma[EL], dg[EL], db[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) {
-        const int c = (e / 8 * TR + t) * 8 + e % 8;
-        gamma[e] = c >= a.cols ? 0.0f : a.gamma ? a.gamma[c] : 1.0f;
+        const int c = vec_start<8>((e / 8 * TR + t) * 8, a.cols) + e % 8;
+        gamma[e] = a.gamma ? a.gamma[c] : 1.0f;
         dg[e] = db[e] = 0.0f;
     }
 
@@ -216,9 +214,9 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
         const int cols = fresh(a.cols);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            const int c = (u * TR + t) * 8;
-            d[u].load(dr + c, cols - c);
-            xx[u].load(xr + c, cols - c);
+            const int c = vec_start<8>((u * TR + t) * 8, cols);
+            d[u].load(dr + c);
+            xx[u].load(xr + c);
         }
         m = a.layer ? a.mean[r] : 0.0f;
         s = a.rstd[r];
@@ -268,10 +266,16 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
             float d[8], v[8];
             ud[u].get(d);
             ux[u].get(v);
+            if ((u + 1) * TR * 8 > cols) {
+                // what is another unit's, or beyond the row, adds nothing
+                const int c = (u * TR + t) * 8, skip = c - vec_start<8>(c, cols);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    d[j] = j >= skip ? d[j] : 0.0f;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int e = u * 8 + j;
-                // beyond the row: gamma and dy are 0
                 const float n = (v[j] - mu) * rs, w = d[j] * gamma[e];
                 su += w;
                 sun = fmaf(w, n, sun);
@@ -311,11 +315,12 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
                     const float n = (v[j] - mu) * rs, w = d[j] * gamma[u * 8 + j];
                     d[j] = rs * (fmaf(-n, mun, w) - muu);
                 }
+                const int from = vec_start<8>(c, cols);
                 if (c < cols) {
                     if (a.dx_dtype == MXQ_OUT_F32)
-                        store_some((float *)a.dx + r * a.ld_dx + c, d, cols - c);
+                        store_from((float *)a.dx + r * a.ld_dx + from, d, c - from);
                     else
-                        store_some((bf16_t *)a.dx + r * a.ld_dx + c, d, cols - c);
+                        store_from((bf16_t *)a.dx + r * a.ld_dx + from, d, c - from);
                 }
             }
         }
@@ -371,14 +376,14 @@ k_norm_sum(const float *part, int64_t groups, int tr, int slots, int cols, float
 #pragma unroll
         for (int k = 0; k < 16; ++k)
             v += lds[k][lane];
-        const int e = s / tr, c = (e / 8 * tr + s % tr) * 8 + e % 8;
-        if (c < cols)
-            out[c] = v;
+        const int e = s / tr, c = (e / 8 * tr + s % tr) * 8, from = vec_start<8>(c, cols);
+        if (e % 8 >= c - from)
+            out[from + e % 8] = v;
     }
 }
 
-// ---- backward of wider rows ------------------------------------------------------------
-// dx a row at a time, the sums a column at a time; dy and x are read once for each.
+// ---- backward of other rows ------------------------------------------------------------
+// Wider rows, and rows shorter than a vector.  dx a row at a time, the sums a column at a time; dy and x are read once for each.
 
 constexpr int kWideNT = 256;
 
@@ -475,7 +480,7 @@ constexpr int64_t kCus = 256;
 BwdPlan plan_bwd(int64_t rows, int64_t cols)
 {
     BwdPlan p = {};
-    if (cols > 16384) {
+    if (cols > 16384 || cols < 8) {
         p.groups = rows < kCus ? rows : kCus;
         p.slots = cols;
         return p;
@@ -556,19 +561,15 @@ extern "C" mxq_status mxq_norm_forward(int32_t kind, const void *x, int32_t x_dt
         using X = std::remove_pointer_t<decltype(xt)>;
         const X *xx = static_cast<const X *>(x);
         hipStream_t s = static_cast<hipStream_t>(stream);
-        // a wave per row while it holds the row in 8 vectors a lane: no barrier
-        if (cols <= 64 * 8 * kElems<X>)
-            hipLaunchKernelGGL((k_norm_fwd<X, 64, 8, false>), dim3(row_grid(rows)), dim3(64), 0, s,
-                               xx, a);
-        else if (cols <= 256 * 8 * kElems<X>)
-            hipLaunchKernelGGL((k_norm_fwd<X, 256, 8, false>), dim3(row_grid(rows)), dim3(256), 0,
-                               s, xx, a);
-        else if (cols <= 1024 * 8 * kElems<X>)
-            hipLaunchKernelGGL((k_norm_fwd<X, 1024, 8, false>), dim3(row_grid(rows)), dim3(1024),
-                               0, s, xx, a);
-        else
-            hipLaunchKernelGGL((k_norm_fwd<X, 1024, 8, true>), dim3(row_grid(rows)), dim3(1024), 0,
-                               s, xx, a);
+        constexpr int64_t one = 64 * 8 * kElems<X>;  // what a wave holds
+        // a wave per row while it holds the row: no barrier
+        const auto k = cols < kElems<X>   ? k_norm_fwd<X, 64, 8, false, true>
+                       : cols <= one      ? k_norm_fwd<X, 64, 8, false, false>
+                       : cols <= 4 * one  ? k_norm_fwd<X, 256, 8, false, false>
+                       : cols <= 16 * one ? k_norm_fwd<X, 1024, 8, false, false>
+                                          : k_norm_fwd<X, 1024, 8, true, false>;
+        const int nt = cols <= one ? 64 : cols <= 4 * one ? 256 : 1024;
+        hipLaunchKernelGGL(k, dim3(row_grid(rows)), dim3(nt), 0, s, xx, a);
     });
     return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_DEVICE;
 }

@@ -79,35 +79,41 @@ template <int E> __device__ __forceinline__ void store_vec(float *p, const float
         *(MXQ_GLOBAL Unaligned<float>::v4 *)(p + j) =
             (gv4u){as_u(f[j]), as_u(f[j + 1]), as_u(f[j + 2]), as_u(f[j + 3])};
 }
-// the first `left` of them (left may be E or more)
+// A row's last vector may be partial.  It is loaded whole, from the row's last E
+// elements, so that a load is the same straight code everywhere (a branch around it
+// would make the compiler wait for all loads in flight): the vector that should start
+// at element `at` of n starts at vec_start, and its first skipped() elements belong to
+// the vector before it (E and more: there is none at `at`).
+template <int E> __device__ __forceinline__ int vec_start(int at, int n) { return min(at, n - E); }
+
+// elements from `skip` on
 template <class O, int E>
-__device__ __forceinline__ void store_some(O *p, const float (&f)[E], int left)
+__device__ __forceinline__ void store_from(O *p, const float (&f)[E], int skip)
 {
-    if (left >= E) {
+    if (skip == 0) {
         store_vec(p, f);
     } else {
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (j < left)
+        for (int j = 1; j < E; ++j)
+            if (j >= skip)
                 *(MXQ_GLOBAL O *)(p + j) = (O)f[j];
     }
 }
 
-// kElems<T> elements of which the first `left` are there; the others are `fill`
-// (a bit pattern of two bf16 or one fp32)
-template <class T> __device__ __forceinline__ gv4u load_some(const T *p, int left, uint32_t fill)
+// The only vector of a row with fewer than kElems<T> elements, as load_vec would give
+// it: element j of it is element j - (kElems<T> - n) of the row.
+template <class T> __device__ __forceinline__ gv4u load_short(const T *p, int n)
 {
-    if (left >= kElems<T>)
-        return load_vec(p);
-    gv4u v = {fill, fill, fill, fill};
+    gv4u v = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int j = 0; j < kElems<T> - 1; ++j) {
-        if (j < left) {
+    for (int j = 1; j < kElems<T>; ++j) {
+        const int e = j - (kElems<T> - n);
+        if (e >= 0) {
             if constexpr (sizeof(T) == 4) {
-                v[j] = *(const MXQ_GLOBAL uint32_t *)(p + j);
+                v[j] = *(const MXQ_GLOBAL uint32_t *)(p + e);
             } else {
-                const uint32_t h = *(const MXQ_GLOBAL uint16_t *)(p + j);
-                v[j / 2] = j % 2 ? (v[j / 2] & 0xFFFFu) | (h << 16) : (v[j / 2] & 0xFFFF0000u) | h;
+                const uint32_t h = *(const MXQ_GLOBAL uint16_t *)(p + e);
+                v[j / 2] |= j % 2 ? h << 16 : h;
             }
         }
     }
@@ -132,26 +138,40 @@ template <int E, class T> __device__ __forceinline__ T *lane_at(T *p)
 
 // ---- a stretch of a row in the registers of a workgroup -------------------------
 // n elements from p, NV vectors a thread: vector i of thread t starts at element
-// (i NT + t) kElems.  What lies beyond n is `fill`.  The whole stretch is in
-// flight at once, and a second pass over it costs no memory traffic.
+// (i NT + t) kElems.  The whole stretch is in flight at once, and a second pass over
+// it costs no memory traffic.  A stretch of fewer than kElems elements has to follow
+// others of its row, or the row is short.
 template <class T, int NT, int NV> struct Held {
     static constexpr int E = kElems<T>;
     static constexpr int kMost = NT * NV * E;
     gv4u v[NV];
 
     static __device__ __forceinline__ int at(int i) { return (i * NT + (int)threadIdx.x) * E; }
+    // whether vector i is there for some thread, for all threads
     static __device__ __forceinline__ bool any(int i, int n) { return i * NT * E < n; }
+    static __device__ __forceinline__ bool whole(int i, int n) { return (i + 1) * NT * E <= n; }
+    // where the thread's vector i starts, and what of it is not its own
+    static __device__ __forceinline__ int start(int i, int n) { return vec_start<E>(at(i), n); }
+    static __device__ __forceinline__ int skip(int i, int n) { return at(i) - start(i, n); }
 
-    __device__ __forceinline__ void load(const T *p, int n, uint32_t fill)
+    __device__ __forceinline__ void load(int i, const T *p, int n)
     {
+        // a uniform address and an unsigned offset: no 64-bit address per vector
+        const int lo = min(0, n - E);
+        v[i] = load_vec((p + lo) + (unsigned)(start(i, n) - lo));
+    }
+    // SHORT: the row has fewer than E elements
+    template <bool SHORT> __device__ __forceinline__ void load(const T *p, int n)
+    {
+        if constexpr (SHORT) {
+            v[0] = load_short(p, n);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if ((i + 1) * NT * E <= n)
-                v[i] = load_vec(lane_at<E>(p + i * NT * E));
-            else if (any(i, n))
-                v[i] = load_some(lane_at<E>(p + i * NT * E), n - at(i), fill);
-            else
-                v[i] = (gv4u){fill, fill, fill, fill};
+            for (int i = 1; i < NV; ++i)
+                v[i] = v[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                load(i, p, n);
         }
     }
     // Before a second pass: what the first one made of the vectors (their unpacked
@@ -163,16 +183,30 @@ template <class T, int NT, int NV> struct Held {
             asm volatile("" : "+v"(v[i]));
     }
     __device__ __forceinline__ void get(int i, float (&f)[E]) const { unpack(v[i], f, (T *)nullptr); }
+    // what is not the thread's own is `none`
+    __device__ __forceinline__ void get(int i, int n, float none, float (&f)[E]) const
+    {
+        get(i, f);
+        if (!whole(i, n)) {
+            const int d = skip(i, n);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                f[j] = j >= d ? f[j] : none;
+        }
+    }
+    // f as vector i of a stretch at o
+    template <class O>
+    static __device__ __forceinline__ void put(O *o, int i, int n, const float (&f)[E])
+    {
+        if (whole(i, n)) {
+            store_vec(lane_at<E>(o + i * NT * E), f);
+        } else {
+            const int d = skip(i, n);
+            if (d < E)
+                store_from(o + start(i, n), f, d);
+        }
+    }
 };
-
-template <class O, int NT, int E>
-__device__ __forceinline__ void store_held(O *p, int i, int n, const float (&f)[E])
-{
-    if ((i + 1) * NT * E <= n)
-        store_vec(lane_at<E>(p + i * NT * E), f);
-    else
-        store_some(lane_at<E>(p + i * NT * E), f, n - (i * NT + (int)threadIdx.x) * E);
-}
 
 // ---- reductions -----------------------------------------------------------------
 __device__ __forceinline__ float wave_sum(float v)

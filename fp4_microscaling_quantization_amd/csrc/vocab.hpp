@@ -13,8 +13,9 @@ namespace mxq {
 // (1024 threads) that is 256 KB, half of a CU's registers: 131072 bf16 or 65536
 // fp32 logits.  Longer rows take several stretches.
 constexpr int kHeld = 16;
-
-template <class T> constexpr uint32_t kMaskedBits = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+// They are taken in groups of 16 elements.
+template <class T> constexpr int kGroup = 16 / kElems<T>;
+template <class T> constexpr int kGroups = kHeld / kGroup<T>;
 
 // What the kernels take of the temperature: 1 / T and log2(e) / T.
 struct Heat {
@@ -46,13 +47,15 @@ __device__ __forceinline__ void move_to(RowStats &st, float to, float log2)
     st.m = to;
 }
 
+// takes the values in, and returns their maximum
 template <bool ENTROPY, int N>
-__device__ __forceinline__ void absorb(RowStats &st, const float (&f)[N], float log2)
+__device__ __forceinline__ float absorb(RowStats &st, const float (&f)[N], float log2)
 {
     float m = f[0];
 #pragma unroll
     for (int j = 1; j < N; ++j)
         m = fmaxf(m, f[j]);
+    const float most = m;
     m = fmaxf(st.m, m);
     const float d = fmaxf((st.m - m) * log2, kFloorLog2);
     const float sc = __builtin_amdgcn_exp2f(d);
@@ -71,29 +74,31 @@ __device__ __forceinline__ void absorb(RowStats &st, const float (&f)[N], float 
     if (ENTROPY)
         st.a += a;
     st.m = m;
+    return most;
 }
 
-// The statistics of n elements at p, into the threads' own states; the held
-// vectors stay in h.  16 elements at a time: what a step costs beside its
-// exponentials is shared by them.
+// The statistics of a held stretch of n elements into the threads' own states, 16
+// elements at a time: what a step costs beside its exponentials is shared by them.
+// most: the maxima of the thread's groups.
 template <bool ENTROPY, class T, int NT>
 __device__ __forceinline__ void absorb_held(RowStats &st, const Held<T, NT, kHeld> &h, int n,
-                                            float log2)
+                                            float log2, float (&most)[kGroups<T>])
 {
-    constexpr int E = kElems<T>, G = 16 / E;
+    constexpr int E = kElems<T>, G = kGroup<T>;
 #pragma unroll
     for (int i = 0; i < kHeld; i += G) {
+        most[i / G] = -INFINITY;
         if (h.any(i, n)) {
             float f[16];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 float part[E];
-                h.get(i + g, part);
+                h.get(i + g, n, -INFINITY, part);
 #pragma unroll
                 for (int j = 0; j < E; ++j)
                     f[g * E + j] = part[j];
             }
-            absorb<ENTROPY>(st, f, log2);
+            most[i / G] = absorb<ENTROPY>(st, f, log2);
         }
     }
 }
@@ -164,17 +169,21 @@ template <class F> void with_type(int32_t d, F f)
         f((bf16_t *)nullptr);
 }
 
-// f(integral constant: threads of a workgroup) for a row of n elements of T: the
-// fewest that hold it, so that short rows share a CU, and the widest beyond.
+// f(integral constants: threads of a workgroup, whether the row is shorter than a
+// vector) for a row of n elements of T: the fewest threads that hold it, so that
+// short rows share a CU, and the widest beyond.
 template <class T, class F> void with_threads(int64_t n, F f)
 {
     constexpr int64_t one = 64 * kHeld * kElems<T>;  // what a wave holds
-    if (n <= 4 * one)
-        f(std::integral_constant<int, 256>());
+    constexpr std::false_type whole;
+    if (n < kElems<T>)
+        f(std::integral_constant<int, 256>(), std::true_type());
+    else if (n <= 4 * one)
+        f(std::integral_constant<int, 256>(), whole);
     else if (n <= 8 * one)
-        f(std::integral_constant<int, 512>());
+        f(std::integral_constant<int, 512>(), whole);
     else
-        f(std::integral_constant<int, 1024>());
+        f(std::integral_constant<int, 1024>(), whole);
 }
 
 // The checks that every call over a vocabulary shares: the logits and the
