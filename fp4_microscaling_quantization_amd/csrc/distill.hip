@@ -83,6 +83,7 @@ __device__ __forceinline__ Gradient distill_gradient(const Teacher &t, float w, 
     return {base_of(st.m), st.s == 0.0f ? 0.0f : w * h.t * t.sum / st.s, 0.0f};
 }
 
+// a held stretch's gradient to o
 template <bool SLOPE, class T, class O, int NT, int NV>
 __device__ __forceinline__ void write_gradient(const Held<T, NT, NV> &held, O *o, int n,
                                                const Gradient &g, float log2)
@@ -140,75 +141,149 @@ __device__ __forceinline__ void write_ids(O *o, const Teacher &t, float zt, int 
 
 // ---- whole rows ----------------------------------------------------------------------
 
-// One workgroup per row: loss (stats where asked for), and with GRADIENT dlogits.
-// Rows longer than the registers hold: the stretches before the last are read
-// again for the gradient, from the last-level cache, where one row per CU stays.
-template <class T, class O, int NT, bool GRADIENT, bool SHORT>
+// The loss (and stats) of a row that counts, by one wave.
+__device__ __forceinline__ void write_loss(float *loss, float *stats, int64_t r, const Teacher &t,
+                                           float zt, float w, int vocab, const RowStats &st,
+                                           const Heat &heat)
+{
+    const float l = row_loss(t, zt, t.id >= 0 && t.id < vocab, w, st, heat);
+    if ((threadIdx.x & 63) == 0) {
+        loss[r] = counts(t, w) ? l : 0.0f;
+        if (stats) {
+            stats[2 * r] = st.m;
+            stats[2 * r + 1] = st.s;
+        }
+    }
+}
+// those of a row with w = 0
+__device__ __forceinline__ void write_no_loss(float *loss, float *stats, int64_t r)
+{
+    if (threadIdx.x == 0) {
+        loss[r] = 0.0f;
+        if (stats) {
+            stats[2 * r] = 0.0f;
+            stats[2 * r + 1] = 1.0f;
+        }
+    }
+}
+// the logit at the lane's id, where that is in [from, to); it is there before the next
+// barrier, behind which the gradient may be written over it
+template <class T>
+__device__ __forceinline__ float logit_at(const T *z, const Teacher &t, int from, int to)
+{
+    float zt = t.id >= from && t.id < to ? load_one(z + t.id) : 0.0f;
+    asm volatile("" : "+v"(zt));
+    return zt;
+}
+
+// One workgroup per row: loss and stats.
+constexpr int kLossNT = 256;
+template <class T, bool SHORT>
+__global__ void __launch_bounds__(kLossNT, 4)
+k_distill_loss(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, TeacherArgs ta,
+               float *loss, float *stats)
+{
+    using H = Held<T, kLossNT, kHeld>;
+    __shared__ float lds[3 * kLossNT / 64];
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T *z = logits + r * ld;
+        const float w = ta.weight ? ta.weight[r] : 1.0f;
+        if (w == 0.0f) {
+            write_no_loss(loss, stats, r);
+            continue;
+        }
+        RowStats st = {-FLT_MAX, 0.0f, 0.0f};
+        for (int at = 0;;) {
+            const int n = min(vocab - at, H::kMost);
+            H held;
+            held.template load<SHORT, true>(z + at, n);
+            float most[kGroups<T>];
+            absorb_held<false>(st, held, n, heat.log2, most);
+            if (vocab - at <= H::kMost)
+                break;
+            at += H::kMost;
+        }
+        st = block_stats<kLossNT>(st, heat.log2, lds);
+        if (threadIdx.x < 64) {
+            const Teacher t = teacher_row(ta, r, vocab);
+            write_loss(loss, stats, r, t, logit_at(z, t, 0, vocab), w, vocab, st, heat);
+        }
+        __syncthreads();
+    }
+}
+
+// The same from the parts of few rows, one wave a row; stats as asked for, or
+// asked for, for the gradient.
+template <class T>
+__global__ void __launch_bounds__(64)
+k_distill_join(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, TeacherArgs ta,
+               Parts parts, float *loss, float *stats)
+{
+    const int64_t r = blockIdx.x;
+    const float w = ta.weight ? ta.weight[r] : 1.0f;
+    if (w == 0.0f) {
+        write_no_loss(loss, stats, r);
+        return;
+    }
+    const T *z = logits + r * ld;
+    const Teacher t = teacher_row(ta, r, vocab);
+    write_loss(loss, stats, r, t, logit_at(z, t, 0, vocab), w, vocab,
+               part_stats(parts, rows, r, heat.log2), heat);
+}
+
+// One workgroup per row: loss and dlogits.  The row is held; of a row longer than the
+// registers hold, the stretches before the last are read again for the gradient, from
+// the last-level cache.
+template <class T, class O, int NT, bool SHORT>
 __global__ void __launch_bounds__(NT, 4)
 k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, TeacherArgs ta,
-               float *loss, float *stats, O *dlogits, int64_t ld_o)
+               float *loss, O *dlogits, int64_t ld_o)
 {
     using H = Held<T, NT, kHeld>;
     __shared__ float lds[3 * NT / 64];
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *z = logits + r * ld;
-        O *o = GRADIENT ? dlogits + r * ld_o : nullptr;
+        O *o = dlogits + r * ld_o;
         const float w = ta.weight ? ta.weight[r] : 1.0f;
         if (w == 0.0f) {
-            if (threadIdx.x == 0) {
-                loss[r] = 0.0f;
-                if (stats) {
-                    stats[2 * r] = 0.0f;
-                    stats[2 * r + 1] = 1.0f;
-                }
-            }
-            if (GRADIENT)
-                write_all<O, NT>(o, vocab, 0.0f);
+            write_no_loss(loss, nullptr, r);
+            write_all<O, NT>(o, vocab, 0.0f);
             continue;
         }
         H held;
         RowStats st = {-FLT_MAX, 0.0f, 0.0f};
-        int first = 0, n = 0;
-        for (int at = 0;;) {
-            n = min(vocab - at, H::kMost);
-            held.template load<SHORT>(z + at, n);
-            float most[kGroups<T>];
-            absorb_held<false>(st, held, n, heat.log2, most);
-            first = at;
-            if (vocab - at <= H::kMost)
-                break;
-            at += H::kMost;
+        int at = 0, n = 0;
+        float most[kGroups<T>];
+        if constexpr (!SHORT) {
+            for (; vocab - at > H::kMost; at += H::kMost) {
+                held.template load<false, false>(z + at, H::kMost);
+                absorb_held<false>(st, held, H::kMost, heat.log2, most);
+            }
         }
+        n = vocab - at;
+        held.template load<SHORT, true>(z + at, n);
+        absorb_held<false>(st, held, n, heat.log2, most);
         const Teacher t = teacher_row(ta, r, vocab);
-        const bool have = t.id >= 0 && t.id < vocab;
-        const float zt = have ? load_one(z + t.id) : 0.0f;
+        const float zt = logit_at(z, t, 0, vocab);
         st = block_stats<NT>(st, heat.log2, lds);
         held.again();
-        const bool count = counts(t, w);
-        if (threadIdx.x < 64) {
-            const float l = row_loss(t, zt, have, w, st, heat);
-            if (threadIdx.x == 0) {
-                loss[r] = count ? l : 0.0f;
-                if (stats) {
-                    stats[2 * r] = st.m;
-                    stats[2 * r + 1] = st.s;
-                }
+        if (threadIdx.x < 64)
+            write_loss(loss, nullptr, r, t, zt, w, vocab, st, heat);
+        if (!counts(t, w)) {
+            write_all<O, NT>(o, vocab, 0.0f);
+        } else {
+            const Gradient g = distill_gradient(t, w, st, heat);
+            for (;;) {
+                write_gradient<false>(held, o + at, n, g, heat.log2);
+                if (at == 0)
+                    break;
+                at -= H::kMost;
+                n = H::kMost;
+                held.template load<SHORT, true>(z + at, n);
             }
-        }
-        if (GRADIENT) {
-            if (!count) {
-                write_all<O, NT>(o, vocab, 0.0f);
-            } else {
-                const Gradient g = distill_gradient(t, w, st, heat);
-                write_gradient<false>(held, o + first, n, g, heat.log2);
-                for (int at = first - H::kMost; at >= 0; at -= H::kMost) {
-                    held.template load<SHORT>(z + at, H::kMost);
-                    write_gradient<false>(held, o + at, H::kMost, g, heat.log2);
-                }
-                __syncthreads();
-                if (threadIdx.x < 64 && !t.bad)
-                    write_ids(o, t, zt, 0, vocab, g, w * heat.t, ta.top_k, heat.log2);
-            }
+            __syncthreads();
+            if (threadIdx.x < 64 && !t.bad)
+                write_ids(o, t, zt, 0, vocab, g, w * heat.t, ta.top_k, heat.log2);
         }
         __syncthreads();
     }
@@ -222,10 +297,13 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
 constexpr int kChunkNT = 256, kChunkNV = 4;
 template <class T> constexpr int kChunk = kChunkNT * kChunkNV * kElems<T>;
 
-template <class T, class O, bool SHORT>
+// PARTS: the rows' statistics come from their parts, and the first chunk's workgroup
+// writes the loss; the gradient must not lie over the logits then.
+template <class T, class O, bool PARTS, bool SHORT>
 __global__ void __launch_bounds__(kChunkNT)
 k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,
-                 TeacherArgs ta, const float *stats, O *dlogits, int64_t ld_o)
+                 TeacherArgs ta, const float *stats, Parts parts, float *loss, O *dlogits,
+                 int64_t ld_o)
 {
     using H = Held<T, kChunkNT, kChunkNV>;
     for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
@@ -235,15 +313,24 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
         O *o = dlogits + r * ld_o;
         const float w = ta.weight ? ta.weight[r] : 1.0f;
         if (w == 0.0f) {
+            if (PARTS && at == 0)
+                write_no_loss(loss, nullptr, r);
             write_all<O, kChunkNT>(o + at, n, 0.0f);
             continue;
         }
         H held;
-        held.template load<SHORT>(z + at, n);
-        const RowStats st = {stats[2 * r], stats[2 * r + 1], 0.0f};
+        held.template load<SHORT, true>(z + at, n);
         const Teacher t = teacher_row(ta, r, vocab);
         const bool mine = t.id >= at && t.id < at + n;
-        const float zt = mine ? load_one(z + t.id) : 0.0f;
+        float zt = logit_at(z, t, at, at + n);
+        RowStats st;
+        if constexpr (PARTS) {
+            st = part_stats(parts, rows, r, heat.log2);
+            if (at == 0 && threadIdx.x < 64)
+                write_loss(loss, nullptr, r, t, logit_at(z, t, 0, vocab), w, vocab, st, heat);
+        } else {
+            st = {stats[2 * r], stats[2 * r + 1], 0.0f};
+        }
         if (!counts(t, w)) {
             write_all<O, kChunkNT>(o + at, n, 0.0f);
             continue;
@@ -273,7 +360,7 @@ k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks,
         const T *z = logits + r * ld;
         O *o = dlogits + r * ld_o + at;
         H held;
-        held.template load<SHORT>(z + at, n);
+        held.template load<SHORT, true>(z + at, n);
         const int token = d_logprob ? tokens[r] : -1;
         const float gl = token < 0 ? 0.0f : token >= vocab ? NAN : d_logprob[r] * heat.inv;
         const float gh = d_entropy ? d_entropy[r] * heat.inv : 0.0f;
@@ -288,7 +375,8 @@ k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks,
             g.k0 = NAN;
         }
         const bool here = token >= at && token < at + n;
-        const float zt = here ? load_one(z + token) : 0.0f;
+        float zt = here ? load_one(z + token) : 0.0f;
+        asm volatile("" : "+v"(zt));
         held.again();
         __syncthreads();
         write_gradient<true>(held, o, n, g, heat.log2);
@@ -307,33 +395,77 @@ mxq_status check_teacher(int64_t rows, const TeacherArgs &t)
     return aligned4(t.ids) && aligned4(t.lps) && aligned4(t.weight) ? MXQ_OK : MXQ_ERR_ALIGN;
 }
 
-template <bool GRADIENT>
-mxq_status launch_rows(const void *logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
-                       const Heat &heat, const TeacherArgs &ta, float *loss, float *stats,
-                       void *dlogits, int32_t o_dtype, int64_t ld_o, hipStream_t s)
-{
-    with_type(dtype, [&](auto *tt) {
-        with_type(o_dtype, [&](auto *ot) {
-            using T = std::remove_pointer_t<decltype(tt)>;
-            using O = std::remove_pointer_t<decltype(ot)>;
-            with_threads<T>(vocab, [&](auto nt, auto is_short) {
-                constexpr int NT = decltype(nt)::value;
-                constexpr bool SHORT = decltype(is_short)::value;
-                hipLaunchKernelGGL((k_distill_rows<T, O, NT, GRADIENT, SHORT>), dim3(row_grid(rows)),
-                                   dim3(NT), 0, s, static_cast<const T *>(logits), ld, rows,
-                                   (int)vocab, heat, ta, loss, stats, static_cast<O *>(dlogits),
-                                   ld_o);
-            });
-        });
-    });
-    return launched();
-}
-
 // the chunks of a row, and the grid of a launch over them
 template <class T> int chunks_of(int64_t vocab) { return (int)((vocab + kChunk<T> - 1) / kChunk<T>); }
 unsigned chunk_grid(int64_t rows, int chunks)
 {
     return (unsigned)(rows < kMaxGrid / chunks ? rows * chunks : kMaxGrid);
+}
+
+// The logits of a call that was checked.
+constexpr int64_t kWholeRows = 256;  // rows from which a workgroup takes a whole one
+struct Logits {
+    const void *z;
+    int32_t dtype;
+    int64_t ld, rows, vocab;
+    Heat heat;
+};
+
+void launch_loss(const Logits &a, const TeacherArgs &ta, float *loss, float *stats, hipStream_t s)
+{
+    with_type(a.dtype, [&](auto *tt) {
+        using T = std::remove_pointer_t<decltype(tt)>;
+        const auto k = a.vocab < kElems<T> ? k_distill_loss<T, true> : k_distill_loss<T, false>;
+        hipLaunchKernelGGL(k, dim3(row_grid(a.rows)), dim3(kLossNT), 0, s,
+                           static_cast<const T *>(a.z), a.ld, a.rows, (int)a.vocab, a.heat, ta,
+                           loss, stats);
+    });
+}
+void launch_join(const Logits &a, const TeacherArgs &ta, const Parts &parts, float *loss,
+                 float *stats, hipStream_t s)
+{
+    with_type(a.dtype, [&](auto *tt) {
+        using T = std::remove_pointer_t<decltype(tt)>;
+        hipLaunchKernelGGL((k_distill_join<T>), dim3((unsigned)a.rows), dim3(64), 0, s,
+                           static_cast<const T *>(a.z), a.ld, a.rows, (int)a.vocab, a.heat, ta,
+                           parts, loss, stats);
+    });
+}
+void launch_rows(const Logits &a, const TeacherArgs &ta, float *loss, void *dlogits,
+                 int32_t o_dtype, int64_t ld_o, hipStream_t s)
+{
+    with_type(a.dtype, [&](auto *tt) {
+        with_type(o_dtype, [&](auto *ot) {
+            using T = std::remove_pointer_t<decltype(tt)>;
+            using O = std::remove_pointer_t<decltype(ot)>;
+            with_threads<T>(a.vocab, [&](auto nt, auto is_short) {
+                constexpr int NT = decltype(nt)::value;
+                constexpr bool SHORT = decltype(is_short)::value;
+                hipLaunchKernelGGL((k_distill_rows<T, O, NT, SHORT>), dim3(row_grid(a.rows)),
+                                   dim3(NT), 0, s, static_cast<const T *>(a.z), a.ld, a.rows,
+                                   (int)a.vocab, a.heat, ta, loss, static_cast<O *>(dlogits),
+                                   ld_o);
+            });
+        });
+    });
+}
+// parts with count > 1: the statistics and the loss from there; else from stats
+void launch_chunks(const Logits &a, const TeacherArgs &ta, const float *stats, const Parts &parts,
+                   float *loss, void *dlogits, int32_t o_dtype, int64_t ld_o, hipStream_t s)
+{
+    with_type(a.dtype, [&](auto *tt) {
+        with_type(o_dtype, [&](auto *ot) {
+            using T = std::remove_pointer_t<decltype(tt)>;
+            using O = std::remove_pointer_t<decltype(ot)>;
+            const int chunks = chunks_of<T>(a.vocab);
+            const auto k = parts.count > 1           ? k_distill_chunks<T, O, true, false>
+                           : a.vocab < kElems<T> ? k_distill_chunks<T, O, false, true>
+                                                     : k_distill_chunks<T, O, false, false>;
+            hipLaunchKernelGGL(k, dim3(chunk_grid(a.rows, chunks)), dim3(kChunkNT), 0, s,
+                               static_cast<const T *>(a.z), a.ld, a.rows, (int)a.vocab, chunks,
+                               a.heat, ta, stats, parts, loss, static_cast<O *>(dlogits), ld_o);
+        });
+    });
 }
 
 }  // namespace
@@ -394,8 +526,16 @@ extern "C" mxq_status mxq_distill_forward(const void *logits, int32_t dtype, int
     const size_t need = mxq_vocab_workspace_size(rows, vocab, 0);
     if (need > 0 && (!workspace || ws_bytes < need))
         return MXQ_ERR_WORKSPACE;
-    return launch_rows<false>(logits, dtype, ld, rows, vocab, heat_of(temperature), ta, loss,
-                              stats, nullptr, MXQ_OUT_F32, 0, static_cast<hipStream_t>(stream));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const Logits a = {logits, dtype, ld, rows, vocab, heat_of(temperature)};
+    const Parts parts = parts_of(rows, vocab, 0, workspace);
+    if (parts.count > 1) {
+        launch_parts(logits, dtype, ld, rows, vocab, a.heat, 0, parts, s);
+        launch_join(a, ta, parts, loss, stats, s);
+    } else {
+        launch_loss(a, ta, loss, stats, s);
+    }
+    return launched();
 }
 
 extern "C" mxq_status mxq_distill_backward(const void *logits, int32_t dtype, int64_t ld,
@@ -418,19 +558,9 @@ extern "C" mxq_status mxq_distill_backward(const void *logits, int32_t dtype, in
         return MXQ_ERR_NULL;
     if (!aligned4(stats))
         return MXQ_ERR_ALIGN;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    with_type(dtype, [&](auto *tt) {
-        with_type(dlogits_dtype, [&](auto *ot) {
-            using T = std::remove_pointer_t<decltype(tt)>;
-            using O = std::remove_pointer_t<decltype(ot)>;
-            const int chunks = chunks_of<T>(vocab);
-            const auto k = vocab < kElems<T> ? k_distill_chunks<T, O, true> : k_distill_chunks<T, O, false>;
-            hipLaunchKernelGGL(k, dim3(chunk_grid(rows, chunks)), dim3(kChunkNT), 0, s,
-                               static_cast<const T *>(logits), ld, rows, (int)vocab, chunks,
-                               heat_of(temperature), ta, stats, static_cast<O *>(dlogits),
-                               ld_dlogits);
-        });
-    });
+    launch_chunks({logits, dtype, ld, rows, vocab, heat_of(temperature)}, ta, stats,
+                  {1, (int)vocab, nullptr, nullptr}, nullptr, dlogits, dlogits_dtype, ld_dlogits,
+                  static_cast<hipStream_t>(stream));
     return launched();
 }
 
@@ -456,7 +586,22 @@ extern "C" mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld,
     const size_t need = mxq_vocab_workspace_size(rows, vocab, 0);
     if (need > 0 && (!workspace || ws_bytes < need))
         return MXQ_ERR_WORKSPACE;
-    return launch_rows<true>(logits, dtype, ld, rows, vocab, heat_of(temperature), ta, loss,
-                             nullptr, dlogits, dlogits_dtype, ld_dlogits,
-                             static_cast<hipStream_t>(stream));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const Logits a = {logits, dtype, ld, rows, vocab, heat_of(temperature)};
+    const Parts parts = parts_of(rows, vocab, 0, workspace);
+    if (parts.count == 1 || rows >= kWholeRows) {
+        launch_rows(a, ta, loss, dlogits, dlogits_dtype, ld_dlogits, s);
+        return launched();
+    }
+    launch_parts(logits, dtype, ld, rows, vocab, a.heat, 0, parts, s);
+    if (dlogits != logits) {
+        launch_chunks(a, ta, nullptr, parts, loss, dlogits, dlogits_dtype, ld_dlogits, s);
+        return launched();
+    }
+    // the loss reads logits of the whole row: before anything is written over them
+    float *stats = parts.stats + 3 * rows * parts.count;
+    launch_join(a, ta, parts, loss, stats, s);
+    launch_chunks(a, ta, stats, {1, (int)vocab, nullptr, nullptr}, nullptr, dlogits, dlogits_dtype,
+                  ld_dlogits, s);
+    return launched();
 }

@@ -243,48 +243,128 @@ __device__ __forceinline__ void write_row(const LogprobOut &out, const T *z, int
     }
 }
 
+// The statistics of n logits at z, entry `first` of their row the first, and wave 0's list
+// of their alternatives.
+template <class T, bool TOP, bool SHORT, class S>
+__device__ __forceinline__ RowStats whole_part(const T *z, int first, int n, int top_k,
+                                               const Heat &heat, float *lds, S &search,
+                                               uint64_t &list)
+{
+    using H = Held<T, kNT, kHeld>;
+    RowStats st = {-FLT_MAX, 0.0f, 0.0f};
+    list = 0;
+    for (int at = 0;;) {
+        const int here = min(n - at, H::kMost);
+        H held;
+        held.template load<SHORT, true>(z + at, here);
+        float most[kGroups<T>];
+        absorb_held<true>(st, held, here, heat.log2, most);
+        if constexpr (TOP)
+            list = top_held(list, held, first + at, here, most, st.m, top_k, search);
+        if (n - at <= H::kMost)
+            break;
+        at += H::kMost;
+    }
+    return block_stats<kNT>(st, heat.log2, lds);
+}
+
 template <class T, bool TOP, bool SHORT>
 __global__ void __launch_bounds__(kNT, 4)
 k_logprobs(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, LogprobOut out)
 {
-    using H = Held<T, kNT, kHeld>;
     __shared__ float lds[3 * kNT / 64];
     __shared__ typename std::conditional<TOP, Search, char>::type search;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *z = logits + r * ld;
-        RowStats st = {-FLT_MAX, 0.0f, 0.0f};
-        uint64_t list = 0;
-        for (int at = 0;;) {
-            const int n = min(vocab - at, H::kMost);
-            H held;
-            held.template load<SHORT>(z + at, n);
-            float most[kGroups<T>];
-            absorb_held<true>(st, held, n, heat.log2, most);
-            if constexpr (TOP)
-                list = top_held(list, held, at, n, most, st.m, out.top_k, search);
-            if (vocab - at <= H::kMost)
-                break;
-            at += H::kMost;
-        }
-        st = block_stats<kNT>(st, heat.log2, lds);
+        uint64_t list;
+        const RowStats st =
+            whole_part<T, TOP, SHORT>(z, 0, vocab, out.top_k, heat, lds, search, list);
         if (threadIdx.x < 64)
             write_row(out, z, r, vocab, st, list, heat);
         __syncthreads();
     }
 }
 
+// one workgroup per part of a row
+template <class T, bool TOP>
+__global__ void __launch_bounds__(kNT, 4)
+k_parts(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, int top_k, Parts parts)
+{
+    __shared__ float lds[3 * kNT / 64];
+    __shared__ typename std::conditional<TOP, Search, char>::type search;
+    const int64_t b = blockIdx.x, r = b / parts.count;
+    const int at = (int)(b - r * parts.count) * parts.length;
+    uint64_t list;
+    const RowStats st = whole_part<T, TOP, false>(logits + r * ld + at, at,
+                                                  min(vocab - at, parts.length), top_k, heat, lds,
+                                                  search, list);
+    if (threadIdx.x == 0) {
+        const int64_t all = rows * parts.count;
+        parts.stats[b] = st.m;
+        parts.stats[all + b] = st.s;
+        parts.stats[2 * all + b] = st.a;
+    }
+    if (TOP && (int)threadIdx.x < top_k)
+        parts.keys[b * top_k + threadIdx.x] = list;
+}
+
+// A row's outputs from its parts: each wave merges a share of the lists, then the waves
+// theirs in a tree.
+constexpr int kJoinNT = 512;
+template <class T>
+__global__ void __launch_bounds__(kJoinNT)
+k_logprobs_join(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, LogprobOut out,
+                Parts parts)
+{
+    constexpr int W = kJoinNT / 64;
+    __shared__ uint64_t lists[W][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t r = blockIdx.x;
+    uint64_t list = 0;
+    if (out.top_k > 0) {
+        for (int p = w; p < parts.count; p += W) {
+            const uint64_t k =
+                lane < out.top_k ? parts.keys[(r * parts.count + p) * out.top_k + lane] : 0;
+            list = p == w ? k : wave_merge(list, k);
+        }
+        for (int half = W / 2; half >= 1; half /= 2) {
+            lists[w][lane] = list;
+            __syncthreads();
+            if (w < half)
+                list = wave_merge(list, lists[w + half][lane]);
+            __syncthreads();
+        }
+    }
+    if (w == 0)
+        write_row(out, logits + r * ld, r, vocab, part_stats(parts, rows, r, heat.log2), list,
+                  heat);
+}
+
 }  // namespace
 
 }  // namespace mxq
+
+void mxq::launch_parts(const void *logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                       const Heat &heat, int32_t top_k, const Parts &parts, hipStream_t s)
+{
+    with_type(dtype, [&](auto *tt) {
+        using T = std::remove_pointer_t<decltype(tt)>;
+        hipLaunchKernelGGL((top_k > 0 ? k_parts<T, true> : k_parts<T, false>),
+                           dim3((unsigned)(rows * parts.count)), dim3(kNT), 0, s,
+                           static_cast<const T *>(logits), ld, rows, (int)vocab, heat, top_k,
+                           parts);
+    });
+}
 
 using namespace mxq;
 
 extern "C" size_t mxq_vocab_workspace_size(int64_t rows, int64_t vocab, int32_t top_k)
 {
-    (void)rows;
-    (void)vocab;
-    (void)top_k;
-    return 0;
+    if (rows < 1 || vocab < 1 || vocab > INT32_MAX || top_k < 0 || top_k > MXQ_TOP_MAX)
+        return 0;
+    const Parts p = parts_of(rows, vocab, top_k, nullptr);
+    // and a row's m and s, joined
+    return p.count == 1 ? 0 : (size_t)rows * (p.count * (8 * (size_t)top_k + 12) + 8);
 }
 
 extern "C" mxq_status mxq_token_logprobs(const void *logits, int32_t dtype, int64_t ld,
@@ -312,8 +392,17 @@ extern "C" mxq_status mxq_token_logprobs(const void *logits, int32_t dtype, int6
         return MXQ_ERR_WORKSPACE;
     const LogprobOut out = {tokens, logprob, entropy, stats, top_k, top_ids, top_logprobs};
     hipStream_t s = static_cast<hipStream_t>(stream);
+    const Parts parts = parts_of(rows, vocab, top_k, workspace);
+    if (parts.count > 1)
+        launch_parts(logits, dtype, ld, rows, vocab, heat_of(temperature), top_k, parts, s);
     with_type(dtype, [&](auto *tt) {
         using T = std::remove_pointer_t<decltype(tt)>;
+        if (parts.count > 1) {
+            hipLaunchKernelGGL((k_logprobs_join<T>), dim3((unsigned)rows), dim3(kJoinNT), 0, s,
+                               static_cast<const T *>(logits), ld, rows, (int)vocab,
+                               heat_of(temperature), out, parts);
+            return;
+        }
         const bool is_short = vocab < kElems<T>;
         const auto k = top_k > 0 ? (is_short ? k_logprobs<T, true, true> : k_logprobs<T, true, false>)
                                  : (is_short ? k_logprobs<T, false, true> : k_logprobs<T, false, false>);

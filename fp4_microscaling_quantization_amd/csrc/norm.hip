@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
         const X *xr = x + r * a.ld_x;
         H h;
         if (!LONG)
-            h.template load<SHORT>(xr, a.cols);
+            h.template load<SHORT, true>(xr, a.cols);
         // f(vector's number, the stretch's first column, its columns)
         const auto each = [&](auto f) {
             const int cols = fresh(a.cols);
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
             for (int at = 0;;) {
                 const int n = min(cols - at, H::kMost);
                 if (LONG)
-                    h.template load<SHORT>(xr + at, n);
+                    h.template load<SHORT, false>(xr + at, n);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     if (!h.any(i, n))
@@ -160,7 +160,7 @@ template <class T> struct Unit {
     {
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            v[k] = load_vec(p + k * kElems<T>);
+            v[k] = load_vec<true>(p + k * kElems<T>);
     }
     // as Held::again
     __device__ __forceinline__ void again()

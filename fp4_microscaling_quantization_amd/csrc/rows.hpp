@@ -34,6 +34,16 @@ template <class T> __device__ __forceinline__ gv4u load_vec(const T *p)
 {
     return *(const MXQ_GLOBAL typename Unaligned<T>::v4 *)p;
 }
+// ONCE: what is not read again leaves the caches to what is (16-byte loads and stores
+// with the non-temporal hint; 4096 x 32000 bf16 logits to gradients: 112 to 101 us).
+template <bool ONCE, class T> __device__ __forceinline__ gv4u load_vec(const T *p)
+{
+    const auto *g = (const MXQ_GLOBAL typename Unaligned<T>::v4 *)p;
+    if constexpr (ONCE)
+        return __builtin_nontemporal_load(g);
+    else
+        return *g;
+}
 template <class T> __device__ __forceinline__ float load_one(const T *p)
 {
     return (float)*(const MXQ_GLOBAL T *)p;
@@ -63,22 +73,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
 }
 
-// E consecutive elements
+// E consecutive elements, not read again here
 template <int E> __device__ __forceinline__ void store_vec(bf16_t *p, const float (&f)[E])
 {
     if constexpr (E == 8)
-        *(MXQ_GLOBAL Unaligned<bf16_t>::v4 *)p = (gv4u){pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                                        pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+        __builtin_nontemporal_store((gv4u){pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                           pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])},
+                                    (MXQ_GLOBAL Unaligned<bf16_t>::v4 *)p);
     else
-        *(MXQ_GLOBAL Unaligned<bf16_t>::v2 *)p = (gv2u){pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+        __builtin_nontemporal_store((gv2u){pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])},
+                                    (MXQ_GLOBAL Unaligned<bf16_t>::v2 *)p);
 }
 template <int E> __device__ __forceinline__ void store_vec(float *p, const float (&f)[E])
 {
 #pragma unroll
     for (int j = 0; j < E; j += 4)
-        *(MXQ_GLOBAL Unaligned<float>::v4 *)(p + j) =
-            (gv4u){as_u(f[j]), as_u(f[j + 1]), as_u(f[j + 2]), as_u(f[j + 3])};
+        __builtin_nontemporal_store(
+            (gv4u){as_u(f[j]), as_u(f[j + 1]), as_u(f[j + 2]), as_u(f[j + 3])},
+            (MXQ_GLOBAL Unaligned<float>::v4 *)(p + j));
 }
+
 // A row's last vector may be partial.  It is loaded whole, from the row's last E
 // elements, so that a load is the same straight code everywhere (a branch around it
 // would make the compiler wait for all loads in flight): the vector that should start
@@ -154,14 +168,8 @@ template <class T, int NT, int NV> struct Held {
     static __device__ __forceinline__ int start(int i, int n) { return vec_start<E>(at(i), n); }
     static __device__ __forceinline__ int skip(int i, int n) { return at(i) - start(i, n); }
 
-    __device__ __forceinline__ void load(int i, const T *p, int n)
-    {
-        // a uniform address and an unsigned offset: no 64-bit address per vector
-        const int lo = min(0, n - E);
-        v[i] = load_vec((p + lo) + (unsigned)(start(i, n) - lo));
-    }
-    // SHORT: the row has fewer than E elements
-    template <bool SHORT> __device__ __forceinline__ void load(const T *p, int n)
+    // SHORT: the row has fewer than E elements; ONCE: it is not read again
+    template <bool SHORT, bool ONCE> __device__ __forceinline__ void load(const T *p, int n)
     {
         if constexpr (SHORT) {
             v[0] = load_short(p, n);
@@ -170,8 +178,11 @@ template <class T, int NT, int NV> struct Held {
                 v[i] = v[0];
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                load(i, p, n);
+            for (int i = 0; i < NV; ++i) {
+                // a uniform address and an unsigned offset: no 64-bit address per vector
+                const int lo = min(0, n - E);
+                v[i] = load_vec<ONCE>((p + lo) + (unsigned)(start(i, n) - lo));
+            }
         }
     }
     // Before a second pass: what the first one made of the vectors (their unpacked

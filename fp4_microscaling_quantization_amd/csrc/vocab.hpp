@@ -85,6 +85,7 @@ __device__ __forceinline__ void absorb_held(RowStats &st, const Held<T, NT, kHel
                                             float log2, float (&most)[kGroups<T>])
 {
     constexpr int E = kElems<T>, G = kGroup<T>;
+    n = fresh(n);
 #pragma unroll
     for (int i = 0; i < kHeld; i += G) {
         most[i / G] = -INFINITY;
@@ -137,10 +138,45 @@ __device__ __forceinline__ RowStats block_stats(RowStats st, float log2, float *
     return all;
 }
 
+// The same over a wave's lanes.
+__device__ __forceinline__ RowStats wave_stats(RowStats st, float log2)
+{
+    move_to(st, wave_max(st.m), log2);
+    st.s = wave_sum(st.s);
+    st.a = wave_sum(st.a);
+    if (st.s == 0.0f)
+        st.m = -INFINITY;
+    return st;
+}
+
 // log q of a logit; -inf throughout a row with every logit masked
 __device__ __forceinline__ float log_q(float z, const RowStats &st, const Heat &h)
 {
     return st.s == 0.0f ? -INFINITY : (z - base_of(st.m)) * h.inv - logf(st.s);
+}
+
+// ---- few rows ----------------------------------------------------------------------
+// A workgroup per row leaves the chip empty when there are few; then several take a
+// part of the row each, and a second launch joins them.  The workspace holds the
+// parts' alternatives, then their m, s and a, each [rows][parts].
+constexpr int kMaxParts = 64;  // a wave joins them
+struct Parts {
+    int count, length;  // parts of a row, logits of a part
+    uint64_t *keys;     // [rows][count][top_k]
+    float *stats;       // [3][rows][count]
+};
+
+// the row's statistics from its parts', in every lane
+__device__ __forceinline__ RowStats part_stats(const Parts &p, int64_t rows, int64_t r, float log2)
+{
+    const int lane = threadIdx.x & 63;
+    const float *f = p.stats + r * p.count + lane;
+    const int64_t all = rows * p.count;
+    RowStats st = {-FLT_MAX, 0.0f, 0.0f};
+    // a part with every logit masked has m = -inf, and must stay at s = 0
+    if (lane < p.count)
+        st = {fmaxf(f[0], -FLT_MAX), f[all], f[2 * all]};
+    return wave_stats(st, log2);
 }
 
 // ---- the host's side -------------------------------------------------------------
@@ -148,6 +184,27 @@ __device__ __forceinline__ float log_q(float z, const RowStats &st, const Heat &
 constexpr int64_t kMaxGrid = 1 << 20;  // workgroups of a launch over rows; more rows loop
 
 inline unsigned row_grid(int64_t rows) { return (unsigned)(rows < kMaxGrid ? rows : kMaxGrid); }
+// Parts so that about 1024 workgroups of 256 threads run, four on a CU; a part has 4096
+// logits at least, below that a workgroup's time is not its loads'.
+inline Parts parts_of(int64_t rows, int64_t vocab, int32_t top_k, void *workspace)
+{
+    int64_t want = rows >= 1024 ? 1 : (1024 + rows - 1) / rows;
+    want = want < vocab / 4096 ? want : vocab / 4096;
+    want = want < kMaxParts ? want : kMaxParts;
+    Parts p = {1, (int)vocab, nullptr, nullptr};
+    if (want > 1) {
+        p.length = (int)(((vocab + want - 1) / want + 15) / 16 * 16);
+        p.count = (int)((vocab + p.length - 1) / p.length);
+        p.keys = static_cast<uint64_t *>(workspace);
+        p.stats = reinterpret_cast<float *>(p.keys + rows * p.count * top_k);
+    }
+    return p;
+}
+// The statistics (and the first top_k alternatives) of all parts of all rows; dtype and
+// sizes were checked.
+void launch_parts(const void *logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                  const Heat &heat, int32_t top_k, const Parts &parts, hipStream_t s);
+
 inline Heat heat_of(float t)
 {
     return {t, (float)(1.0 / (double)t), (float)(1.4426950408889634 / (double)t)};
