@@ -25,31 +25,32 @@ struct FwdArgs {
     float *mean, *rstd;
 };
 
-// n gamma + beta of the E columns from c on; rows shorter than a vector start at a
+// gamma and beta of the E columns from c on; rows shorter than a vector start at a
 // negative c
 template <bool SHORT, int E>
-__device__ __forceinline__ void affine(float (&f)[E], const FwdArgs &a, int c)
+__device__ __forceinline__ void affine(float (&g)[E], float (&b)[E], const FwdArgs &a, int c)
 {
-    if (SHORT) {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (c + j >= 0)
-                f[j] = f[j] * (a.gamma ? a.gamma[c + j] : 1.0f) + (a.beta ? a.beta[c + j] : 0.0f);
-        return;
-    }
 #pragma unroll
     for (int j = 0; j < E; j += 4) {
-        if (a.gamma) {
-            const gv4u v = load_vec(a.gamma + c + j);
+        gv4u vg = {0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u}, vb = {0u, 0u, 0u, 0u};
+        if constexpr (SHORT) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                f[j + k] *= as_f(v[k]);
+            for (int k = 0; k < 4; ++k) {
+                if (c + j + k >= 0) {
+                    vg[k] = a.gamma ? as_u(a.gamma[c + j + k]) : vg[k];
+                    vb[k] = a.beta ? as_u(a.beta[c + j + k]) : vb[k];
+                }
+            }
+        } else {
+            if (a.gamma)
+                vg = load_vec(a.gamma + c + j);
+            if (a.beta)
+                vb = load_vec(a.beta + c + j);
         }
-        if (a.beta) {
-            const gv4u v = load_vec(a.beta + c + j);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                f[j + k] += as_f(v[k]);
+        for (int k = 0; k < 4; ++k) {
+            g[j + k] = as_f(vg[k]);
+            b[j + k] = as_f(vb[k]);
         }
     }
 }
@@ -62,34 +63,43 @@ template <int NT> __device__ __forceinline__ float row_sum(float v, float *lds)
         return block_sum<NT>(v, lds);
 }
 
-// One workgroup per row, NT x NV vectors of it in registers; a longer row (LONG)
-// is read again for each of the three passes.  The variance is the mean square of
-// the differences from the mean, a second pass over registers: mean(x^2) - mu^2
-// loses what the two have in common.
-template <class X, int NT, int NV, bool LONG, bool SHORT>
+// R rows a workgroup, NT x NV vectors of each in registers; a longer row (LONG, R = 1) is
+// read again for each of the three passes.  The variance is the mean square of the
+// differences from the mean, a second pass over registers: mean(x^2) - mu^2 loses
+// what the two have in common.  Two rows share the loads of gamma and beta, which for
+// a bf16 row are four times its own bytes (from L2: the row streams through L1).
+template <class X, int NT, int NV, int R, bool LONG, bool SHORT>
 __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
 {
     using H = Held<X, NT, NV>;
     constexpr int E = kElems<X>;
     __shared__ float lds[NT / 64];
     const float inv = 1.0f / (float)a.cols;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const X *xr = x + r * a.ld_x;
-        H h;
-        if (!LONG)
-            h.template load<SHORT, true>(xr, a.cols);
+    for (int64_t first = (int64_t)blockIdx.x * R; first < a.rows; first += (int64_t)gridDim.x * R) {
+        // an odd last row is worked on R times, and written once
+        const X *xr[R];
+        H h[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            xr[q] = x + (first + q < a.rows ? first + q : first) * a.ld_x;
+            if (!LONG)
+                h[q].template load<SHORT, true>(xr[q], a.cols);
+        }
         // f(vector's number, the stretch's first column, its columns)
         const auto each = [&](auto f) {
             const int cols = fresh(a.cols);
-            if (!LONG)
-                h.again();
+            if (!LONG) {
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    h[q].again();
+            }
             for (int at = 0;;) {
                 const int n = min(cols - at, H::kMost);
                 if (LONG)
-                    h.template load<SHORT, false>(xr + at, n);
+                    h[0].template load<SHORT, false>(xr[0] + at, n);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    if (!h.any(i, n))
+                    if (!H::any(i, n))
                         break;
                     f(i, at, n);
                 }
@@ -98,44 +108,67 @@ __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
                 at += H::kMost;
             }
         };
-        float mu = 0.0f;
+        float mu[R], rs[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            mu[q] = rs[q] = 0.0f;
         if (a.layer) {
-            float s = 0.0f;
             each([&](int i, int, int n) {
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    float v[E];
+                    h[q].get(i, n, 0.0f, v);
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        mu[q] += v[j];
+                }
+            });
+#pragma unroll
+            for (int q = 0; q < R; ++q)
+                mu[q] = row_sum<NT>(mu[q], lds) * inv;
+        }
+        each([&](int i, int, int n) {
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
                 float v[E];
-                h.get(i, n, 0.0f, v);
+                h[q].get(i, n, mu[q], v);
 #pragma unroll
                 for (int j = 0; j < E; ++j)
-                    s += v[j];
-            });
-            mu = row_sum<NT>(s, lds) * inv;
-        }
-        float s2 = 0.0f;
-        each([&](int i, int, int n) {
-            float v[E];
-            h.get(i, n, mu, v);
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                s2 = fmaf(v[j] - mu, v[j] - mu, s2);
+                    rs[q] = fmaf(v[j] - mu[q], v[j] - mu[q], rs[q]);
+            }
         });
-        const float rs = 1.0f / sqrtf(row_sum<NT>(s2, lds) * inv + a.eps);
-        each([&](int i, int at, int n) {
-            float v[E];
-            h.get(i, v);
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                v[j] = (v[j] - mu) * rs;
-            affine<SHORT>(v, a, at + h.start(i, n));
-            if (a.y_dtype == MXQ_OUT_F32)
-                h.put((float *)a.y + r * a.ld_y + at, i, n, v);
-            else
-                h.put((bf16_t *)a.y + r * a.ld_y + at, i, n, v);
+        for (int q = 0; q < R; ++q)
+            rs[q] = 1.0f / sqrtf(row_sum<NT>(rs[q], lds) * inv + a.eps);
+        each([&](int i, int at, int n) {
+            float g[E], b[E];
+            affine<SHORT>(g, b, a, at + H::start(i, n));
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                if (q > 0 && first + q >= a.rows)
+                    break;
+                float v[E];
+                h[q].get(i, v);
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    v[j] = (v[j] - mu[q]) * rs[q] * g[j] + b[j];
+                const int64_t to = (first + q) * a.ld_y + at;
+                if (a.y_dtype == MXQ_OUT_F32)
+                    H::put((float *)a.y + to, i, n, v);
+                else
+                    H::put((bf16_t *)a.y + to, i, n, v);
+            }
         });
         if (threadIdx.x == 0) {
-            if (a.mean && a.layer)
-                a.mean[r] = mu;
-            if (a.rstd)
-                a.rstd[r] = rs;
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                if (first + q >= a.rows)
+                    break;
+                if (a.mean && a.layer)
+                    a.mean[first + q] = mu[q];
+                if (a.rstd)
+                    a.rstd[first + q] = rs[q];
+            }
         }
     }
 }
@@ -152,88 +185,96 @@ struct BwdArgs {
     float *part;  // NULL: no sums over the rows
 };
 
-// 8 consecutive elements of a row, of either type
-template <class T> struct Unit {
-    static constexpr int V = 8 / kElems<T>;
-    gv4u v[V];
+// U consecutive elements of a row: a vector, or half of a bf16 one (U = 4)
+template <class T, int U> struct Unit {
+    using V = typename std::conditional<U * sizeof(T) == 16, gv4u, gv2u>::type;
+    V v;
     __device__ __forceinline__ void load(const T *p)
     {
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            v[k] = load_vec<true>(p + k * kElems<T>);
+        if constexpr (sizeof(V) == 16)
+            v = load_vec<true>(p);
+        else
+            v = __builtin_nontemporal_load((const MXQ_GLOBAL typename Unaligned<T>::v2 *)p);
     }
+    __device__ __forceinline__ void clear() { v = V(0u); }
     // as Held::again
-    __device__ __forceinline__ void again()
+    __device__ __forceinline__ void again() { asm volatile("" : "+v"(v)); }
+    __device__ __forceinline__ void get(float (&f)[U]) const
     {
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            asm volatile("" : "+v"(v[k]));
-    }
-    __device__ __forceinline__ void get(float (&f)[8]) const
-    {
-        if constexpr (V == 1) {
-            unpack(v[0], f, (T *)nullptr);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                f[k] = as_f(v[k / 4][k % 4]);
+        for (int j = 0; j < U; ++j) {
+            if constexpr (sizeof(T) == 4)
+                f[j] = as_f(v[j]);
+            else
+                f[j] = as_f(j % 2 ? v[j / 2] & 0xFFFF0000u : v[j / 2] << 16);
         }
     }
 };
 
 // NT threads as NT / TR groups, each on a row of its own: thread t of a group has
-// the NU units (u TR + t) of 8 columns, for every row that the workgroup takes.  So
+// the units (u TR + t) of U columns, 16 in all, for every row that the workgroup takes.  So
 // gamma, and the sums over the rows of dy n and dy, stay in its registers, and dy
 // and x come from memory once for dx and the sums together.  The next row is
-// loaded before the present one is worked on, where the registers have room.
+// loaded before the present one is worked on.  With 1024 threads there are 128 registers:
+// gamma is in LDS then, and a row is loaded in its turn.
 // One barrier a row: the row's two sums go through alternating places in LDS.
-template <class D, class X, int NT, int TR, int NU>
+constexpr int kOwn = 16;  // columns of a thread
+template <class D, class X> constexpr int kUnit = sizeof(D) + sizeof(X) == 4 ? 8 : 4;
+
+template <class D, class X, int NT, int TR>
 __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X *x, BwdArgs a)
 {
-    constexpr int G = NT / TR, W = TR / 64, EL = 8 * NU;
-    constexpr bool kAhead = NU * 4 * (Unit<D>::V + Unit<X>::V) <= 64;
+    constexpr int G = NT / TR, W = TR / 64, EL = kOwn, U = kUnit<D, X>, NU = EL / U;
+    constexpr bool kAhead = NT < 1024, kLdsGamma = NT == 1024;
     __shared__ float lds[2][2][NT / 64];
     __shared__ float sums[G > 1 ? EL * NT : 1];
+    __shared__ gv4u gammas[kLdsGamma ? EL / 4 : 1][kLdsGamma ? TR : 1];
     const int t = threadIdx.x % TR, g = threadIdx.x / TR, wave = threadIdx.x / 64;
     const float inv = 1.0f / (float)a.cols;
 
-    float gamma[EL], dg[EL], db[EL];
+    float gamma[kLdsGamma ? 1 : EL], dg[EL], db[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) {
-        const int c = vec_start<8>((e / 8 * TR + t) * 8, a.cols) + e % 8;
-        gamma[e] = a.gamma ? a.gamma[c] : 1.0f;
+        const int c = vec_start<U>((e / U * TR + t) * U, a.cols) + e % U;
+        const float v = a.gamma ? a.gamma[c] : 1.0f;
+        if constexpr (kLdsGamma)
+            gammas[e / 4][t][e % 4] = as_u(v);  // read by the same thread only
+        else
+            gamma[e] = v;
         dg[e] = db[e] = 0.0f;
     }
-
-    Unit<D> ud[NU], nd[kAhead ? NU : 1];
-    Unit<X> ux[NU], nx[kAhead ? NU : 1];
-    float mu = 0.0f, rs = 0.0f, nmu = 0.0f, nrs = 0.0f;
-    const auto load = [&](int64_t r, Unit<D> *d, Unit<X> *xx, float &m, float &s) {
-        const D *dr = dy + r * a.ld_dy;
-        const X *xr = x + r * a.ld_x;
-        const int cols = fresh(a.cols);
+    const auto gamma_of = [&](int u, float (&out)[U]) {
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            const int c = vec_start<8>((u * TR + t) * 8, cols);
-            d[u].load(dr + c);
-            xx[u].load(xr + c);
+        for (int j = 0; j < U; ++j) {
+            if constexpr (kLdsGamma)
+                out[j] = as_f(gammas[(u * U + j) / 4][t][j % 4]);
+            else
+                out[j] = gamma[u * U + j];
         }
-        m = a.layer ? a.mean[r] : 0.0f;
-        s = a.rstd[r];
     };
+
+    Unit<D, U> ud[NU], nd[kAhead ? NU : 1];
+    Unit<X, U> ux[NU], nx[kAhead ? NU : 1];
+    float mu = 0.0f, rs = 0.0f, nmu = 0.0f, nrs = 0.0f;
     // a row beyond the last: rstd and dy are 0, so that nothing is added
-    const auto load_or_none = [&](int64_t r, Unit<D> *d, Unit<X> *xx, float &m, float &s) {
+    const auto load_or_none = [&](int64_t r, Unit<D, U> *d, Unit<X, U> *xx, float &m, float &s) {
         if (r < a.rows) {
-            load(r, d, xx, m, s);
+            const D *dr = dy + r * a.ld_dy;
+            const X *xr = x + r * a.ld_x;
+            const int cols = fresh(a.cols);
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                const int c = vec_start<U>((u * TR + t) * U, cols);
+                d[u].load(dr + c);
+                xx[u].load(xr + c);
+            }
+            m = a.layer ? a.mean[r] : 0.0f;
+            s = a.rstd[r];
         } else {
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-#pragma unroll
-                for (int k = 0; k < Unit<D>::V; ++k)
-                    d[u].v[k] = (gv4u){0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int k = 0; k < Unit<X>::V; ++k)
-                    xx[u].v[k] = (gv4u){0u, 0u, 0u, 0u};
+                d[u].clear();
+                xx[u].clear();
             }
             m = s = 0.0f;
         }
@@ -263,20 +304,21 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
         float su = 0.0f, sun = 0.0f;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            float d[8], v[8];
+            float d[U], v[U], gu[U];
             ud[u].get(d);
             ux[u].get(v);
-            if ((u + 1) * TR * 8 > cols) {
+            gamma_of(u, gu);
+            if ((u + 1) * TR * U > cols) {
                 // what is another unit's, or beyond the row, adds nothing
-                const int c = (u * TR + t) * 8, skip = c - vec_start<8>(c, cols);
+                const int c = (u * TR + t) * U, skip = c - vec_start<U>(c, cols);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < U; ++j)
                     d[j] = j >= skip ? d[j] : 0.0f;
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = u * 8 + j;
-                const float n = (v[j] - mu) * rs, w = d[j] * gamma[e];
+            for (int j = 0; j < U; ++j) {
+                const int e = u * U + j;
+                const float n = (v[j] - mu) * rs, w = d[j] * gu[j];
                 su += w;
                 sun = fmaf(w, n, sun);
                 dg[e] = fmaf(d[j], n, dg[e]);
@@ -304,18 +346,19 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
         if (r < a.rows) {
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-                const int c = (u * TR + t) * 8;
-                float d[8], v[8];
+                const int c = (u * TR + t) * U;
+                float d[U], v[U], gu[U];
+                gamma_of(u, gu);
                 ud[u].again();
                 ux[u].again();
                 ud[u].get(d);
                 ux[u].get(v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float n = (v[j] - mu) * rs, w = d[j] * gamma[u * 8 + j];
+                for (int j = 0; j < U; ++j) {
+                    const float n = (v[j] - mu) * rs, w = d[j] * gu[j];
                     d[j] = rs * (fmaf(-n, mun, w) - muu);
                 }
-                const int from = vec_start<8>(c, cols);
+                const int from = vec_start<U>(c, cols);
                 if (c < cols) {
                     if (a.dx_dtype == MXQ_OUT_F32)
                         store_from((float *)a.dx + r * a.ld_dx + from, d, c - from);
@@ -356,14 +399,14 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
 // dgamma and dbeta (blockIdx.y) from the workgroups' sums: 64 slots a workgroup,
 // its 16 waves on a sixteenth of the sums each.
 __global__ void __launch_bounds__(1024)
-k_norm_sum(const float *part, int64_t groups, int tr, int slots, int cols, float *dgamma,
+k_norm_sum(const float *part, int64_t groups, int tr, int unit, int cols, float *dgamma,
            float *dbeta)
 {
     __shared__ float lds[16][64];
     float *out = blockIdx.y ? dbeta : dgamma;
     if (!out)
         return;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, slots = tr * kOwn;
     const int s = blockIdx.x * 64 + lane;
     const float *p = part + blockIdx.y * groups * slots + s;
     float v = 0.0f;
@@ -376,9 +419,9 @@ k_norm_sum(const float *part, int64_t groups, int tr, int slots, int cols, float
 #pragma unroll
         for (int k = 0; k < 16; ++k)
             v += lds[k][lane];
-        const int e = s / tr, c = (e / 8 * tr + s % tr) * 8, from = vec_start<8>(c, cols);
-        if (e % 8 >= c - from)
-            out[from + e % 8] = v;
+        const int e = s / tr, c = (e / unit * tr + s % tr) * unit, from = min(c, cols - unit);
+        if (e % unit >= c - from)
+            out[from + e % unit] = v;
     }
 }
 
@@ -467,69 +510,49 @@ template <class F> void with_type(int32_t d, F f)
         f((bf16_t *)nullptr);
 }
 
-// How the backward pass lays a problem out.  tr threads of a row hold 16 columns
-// each, 32 for rows over 8192; the workgroups are those that fill the chip once.
-// Few rows: workgroups of 256 threads spread them over more CUs.
+constexpr int64_t kTwoRows = 4096;  // rows from which a wave takes two
+
+// How the backward pass lays a problem out.  tr threads of a row hold 16 columns each;
+// the workgroups are those that fill the chip once.  Few rows: workgroups of 256 threads
+// spread them over more CUs.
 struct BwdPlan {
-    int nt, tr, nu;      // nt 0: the wide kernels
-    int64_t groups;      // workgroups (wide: strips), each with a set of sums
-    int64_t slots;       // sums of a set
+    int nt, tr;      // nt 0: the kernels for other rows
+    int64_t groups;  // workgroups (other rows: strips), each with a set of sums
+    int64_t slots;   // sums of a set
 };
 constexpr int64_t kCus = 256;
 
 BwdPlan plan_bwd(int64_t rows, int64_t cols)
 {
     BwdPlan p = {};
-    if (cols > 16384 || cols < 8) {
+    if (cols > 1024 * kOwn || cols < 8) {
         p.groups = rows < kCus ? rows : kCus;
         p.slots = cols;
         return p;
     }
-    p.nu = cols > 8192 ? 4 : 2;
     p.tr = 64;
-    while ((int64_t)p.tr * 8 * p.nu < cols)
+    while ((int64_t)p.tr * kOwn < cols)
         p.tr *= 2;
-    p.nt = p.tr <= 256 && rows < kCus * (512 / p.tr) ? 256 : 512;
+    p.nt = p.tr > 512 ? 1024 : p.tr <= 256 && rows < kCus * (512 / p.tr) ? 256 : 512;
     const int64_t per = p.nt / p.tr, need = (rows + per - 1) / per;
     const int64_t most = p.nt == 256 ? 2 * kCus : kCus;
     p.groups = need < most ? need : most;
-    p.slots = (int64_t)p.tr * 8 * p.nu;
+    p.slots = (int64_t)p.tr * kOwn;
     return p;
 }
 
 template <class D, class X>
 void launch_bwd(const BwdPlan &p, const D *dy, const X *x, const BwdArgs &a, hipStream_t s)
 {
-    const auto go = [&](auto nt, auto tr, auto nu) {
-        constexpr int NT = decltype(nt)::value, TR = decltype(tr)::value, NU = decltype(nu)::value;
-        hipLaunchKernelGGL((k_norm_bwd<D, X, NT, TR, NU>), dim3((unsigned)p.groups), dim3(NT), 0,
-                           s, dy, x, a);
-    };
-    using i2 = std::integral_constant<int, 2>;
-    using i4 = std::integral_constant<int, 4>;
-    using i64 = std::integral_constant<int, 64>;
-    using i128 = std::integral_constant<int, 128>;
-    using i256 = std::integral_constant<int, 256>;
-    using i512 = std::integral_constant<int, 512>;
-    if (p.nt == 256) {
-        if (p.tr == 64)
-            go(i256(), i64(), i2());
-        else if (p.tr == 128)
-            go(i256(), i128(), i2());
-        else
-            go(i256(), i256(), i2());
-    } else if (p.nu == 4) {
-        go(i512(), i512(), i4());
-    } else {
-        if (p.tr == 64)
-            go(i512(), i64(), i2());
-        else if (p.tr == 128)
-            go(i512(), i128(), i2());
-        else if (p.tr == 256)
-            go(i512(), i256(), i2());
-        else
-            go(i512(), i512(), i2());
-    }
+    const auto k = p.nt == 1024  ? k_norm_bwd<D, X, 1024, 1024>
+                   : p.nt == 512 ? (p.tr == 64    ? k_norm_bwd<D, X, 512, 64>
+                                    : p.tr == 128 ? k_norm_bwd<D, X, 512, 128>
+                                    : p.tr == 256 ? k_norm_bwd<D, X, 512, 256>
+                                                  : k_norm_bwd<D, X, 512, 512>)
+                                 : (p.tr == 64    ? k_norm_bwd<D, X, 256, 64>
+                                    : p.tr == 128 ? k_norm_bwd<D, X, 256, 128>
+                                                  : k_norm_bwd<D, X, 256, 256>);
+    hipLaunchKernelGGL(k, dim3((unsigned)p.groups), dim3(p.nt), 0, s, dy, x, a);
 }
 
 }  // namespace
@@ -562,14 +585,16 @@ extern "C" mxq_status mxq_norm_forward(int32_t kind, const void *x, int32_t x_dt
         const X *xx = static_cast<const X *>(x);
         hipStream_t s = static_cast<hipStream_t>(stream);
         constexpr int64_t one = 64 * 8 * kElems<X>;  // what a wave holds
-        // a wave per row while it holds the row: no barrier
-        const auto k = cols < kElems<X>   ? k_norm_fwd<X, 64, 8, false, true>
-                       : cols <= one      ? k_norm_fwd<X, 64, 8, false, false>
-                       : cols <= 4 * one  ? k_norm_fwd<X, 256, 8, false, false>
-                       : cols <= 16 * one ? k_norm_fwd<X, 1024, 8, false, false>
-                                          : k_norm_fwd<X, 1024, 8, true, false>;
+        // a wave per row while it holds the row: no barrier; two rows when there are enough
+        const bool two = cols >= kElems<X> && cols <= one && rows >= kTwoRows;
+        const auto k = cols < kElems<X>   ? k_norm_fwd<X, 64, 8, 1, false, true>
+                       : two              ? k_norm_fwd<X, 64, 8, 2, false, false>
+                       : cols <= one      ? k_norm_fwd<X, 64, 8, 1, false, false>
+                       : cols <= 4 * one  ? k_norm_fwd<X, 256, 8, 1, false, false>
+                       : cols <= 16 * one ? k_norm_fwd<X, 1024, 8, 1, false, false>
+                                          : k_norm_fwd<X, 1024, 8, 1, true, false>;
         const int nt = cols <= one ? 64 : cols <= 4 * one ? 256 : 1024;
-        hipLaunchKernelGGL(k, dim3(row_grid(rows)), dim3(nt), 0, s, xx, a);
+        hipLaunchKernelGGL(k, dim3(row_grid(two ? (rows + 1) / 2 : rows)), dim3(nt), 0, s, xx, a);
     });
     return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_DEVICE;
 }
@@ -635,7 +660,8 @@ extern "C" mxq_status mxq_norm_backward(int32_t kind, const void *dy, int32_t dy
         });
     if (sums && p.nt)
         hipLaunchKernelGGL(k_norm_sum, dim3((unsigned)(p.slots / 64), 2), dim3(1024), 0, s, part,
-                           p.groups, p.tr, (int)p.slots, (int)cols, dgamma, dbeta);
+                           p.groups, p.tr, dy_dtype == MXQ_OUT_BF16 && x_dtype == MXQ_OUT_BF16 ? 8 : 4,
+                           (int)cols, dgamma, dbeta);
     else if (sums)
         hipLaunchKernelGGL(k_norm_wide_sum, dim3(wide, 2), dim3(kWideNT), 0, s, part, p.groups,
                            p.slots, (int)cols, dgamma, dbeta);

@@ -130,8 +130,8 @@ def _check(fn: str, status: int):
         raise MxqError(fn, status)
 
 
-def _ptr(t) -> C.c_void_p | None:
-    return None if t is None else C.c_void_p(t.data_ptr())
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
@@ -513,8 +513,8 @@ def _matrix(name, t, like=None):
     if t.dim() != 2 or (like is not None and t.shape != like.shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}" + (f", not {tuple(like.shape)}" if like is not None else " is not 2-D"))
     rows, cols = t.shape
-    ld = t.stride(0)
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and ld < cols):
+    ld, inner = t.stride()
+    if (cols > 1 and inner != 1) or (rows > 1 and ld < cols):
         raise ValueError(f"{name}: rows must be contiguous and apart (strides {t.stride()})")
     if like is not None and t.device != like.device:
         raise ValueError(f"{name}: on {t.device}, not {like.device}")
@@ -523,56 +523,57 @@ def _matrix(name, t, like=None):
 
 def _vector(name, t, shape, like, dtype=None):
     """Address of a packed fp32 (or `dtype`) tensor of this shape, None for None."""
-    import torch
     if t is None:
         return None
-    if t.dtype != (dtype or torch.float32) or tuple(t.shape) != shape or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"{name}: packed {dtype or torch.float32} of shape {shape} on {like.device} expected, "
+    if dtype is None:
+        import torch
+        dtype = torch.float32
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name}: packed {dtype} of shape {shape} on {like.device} expected, "
                          f"not {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-class _On:
-    """The device and stream of a call: outputs and workspaces are allocated on
-    the stream that uses them, so that their memory is not handed on early."""
+_torch = None
 
-    def __init__(self, x, stream):
+
+def _enter(x, stream):
+    """(torch, handle of the call's stream) for a call on x's device."""
+    global _torch
+    if _torch is None:
         import torch
-        if not x.is_cuda:
-            raise ValueError("GPU tensors expected")
-        if x.device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
-        self.torch, self.device, self.stream = torch, x.device, stream
-        self.handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+        _torch = torch
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("GPU tensors expected")
+    if index != _torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{_torch.cuda.current_device()}")
+    return _torch, _torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
-        with self.torch.cuda.stream(self.stream):
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
 
-    def workspace(self, size):
-        """(tensor, address, bytes); the tensor has to live until the call is enqueued."""
-        if not size:
-            return None, None, 0
-        ws = self.empty((size,), self.torch.uint8)
-        return ws, ws.data_ptr(), size
+def _new(x, shape, dtype, stream):
+    """A packed tensor on x's device, allocated on the stream that uses it, so
+    that its memory is not handed on early."""
+    if stream is None:
+        return x.new_empty(shape, dtype=dtype)
+    with _torch.cuda.stream(stream):
+        return x.new_empty(shape, dtype=dtype)
 
 
 def norm_forward(x, gamma=None, beta=None, *, eps, kind=NORM_LAYER, out_dtype=None, out=None, stream=None):
     """mxq_norm_forward: (y, mean, rstd); mean is None for NORM_RMS.  y has x's
     dtype unless out_dtype says otherwise, or is `out` (x itself serves)."""
-    on = _On(x, stream)
-    f32 = on.torch.float32
+    torch, handle = _enter(x, stream)
+    f32 = torch.float32
     rows, cols = x.shape
-    y = on.empty((rows, cols), out_dtype or x.dtype) if out is None else out
+    y = _new(x, (rows, cols), out_dtype or x.dtype, stream) if out is None else out
     xp, xt, ldx = _matrix("x", x)
     yp, yt, ldy = _matrix("out", y, x)
-    mean = on.empty((rows,), f32) if kind == NORM_LAYER else None
-    rstd = on.empty((rows,), f32)
+    mean = _new(x, (rows,), f32, stream) if kind == NORM_LAYER else None
+    rstd = _new(x, (rows,), f32, stream)
     _check("mxq_norm_forward", lib().mxq_norm_forward(
         kind, xp, xt, ldx, rows, cols, _vector("gamma", gamma, (cols,), x),
-        _vector("beta", beta, (cols,), x), eps, yp, yt, ldy, _ptr(mean), _ptr(rstd), on.handle))
+        _vector("beta", beta, (cols,), x), eps, yp, yt, ldy, _ptr(mean), _ptr(rstd), handle))
     return y, mean, rstd
 
 
@@ -581,22 +582,22 @@ def norm_backward(dy, x, gamma, mean, rstd, *, kind=NORM_LAYER, weight=True, bia
     """mxq_norm_backward: (dx, dgamma, dbeta); dgamma without `weight` and dbeta
     without `bias` are None.  dx has x's dtype unless out_dtype says otherwise,
     or is `out` (dy or x itself serves)."""
-    on = _On(x, stream)
-    f32 = on.torch.float32
+    torch, handle = _enter(x, stream)
+    f32 = torch.float32
     rows, cols = x.shape
-    dx = on.empty((rows, cols), out_dtype or x.dtype) if out is None else out
+    dx = _new(x, (rows, cols), out_dtype or x.dtype, stream) if out is None else out
     xp, xt, ldx = _matrix("x", x)
     dp, dt, ldd = _matrix("dy", dy, x)
     op, ot, ldo = _matrix("out", dx, x)
-    dgamma = on.empty((cols,), f32) if weight else None
-    dbeta = on.empty((cols,), f32) if bias else None
+    dgamma = _new(x, (cols,), f32, stream) if weight else None
+    dbeta = _new(x, (cols,), f32, stream) if bias else None
     size = lib().mxq_norm_backward_workspace_size(rows, cols) if weight or bias else 0
-    ws, wp, size = on.workspace(size)
+    ws = _new(x, (size,), torch.uint8, stream) if size else None
     _check("mxq_norm_backward", lib().mxq_norm_backward(
         kind, dp, dt, ldd, xp, xt, ldx, rows, cols, _vector("gamma", gamma, (cols,), x),
         _vector("mean", mean if kind == NORM_LAYER else None, (rows,), x),
-        _vector("rstd", rstd, (rows,), x), op, ot, ldo, _ptr(dgamma), _ptr(dbeta), wp, size,
-        on.handle))
+        _vector("rstd", rstd, (rows,), x), op, ot, ldo, _ptr(dgamma), _ptr(dbeta), _ptr(ws), size,
+        handle))
     return dx, dgamma, dbeta
 
 
@@ -604,19 +605,20 @@ def token_logprobs(logits, tokens=None, *, top_k=0, temperature=1, entropy=True,
     """mxq_token_logprobs: [logprob, entropy, stats], and top_ids, top_logprobs
     after them where top_k > 0; logprob is None without tokens (int32), entropy
     where it is not asked for."""
-    on = _On(logits, stream)
-    f32, i32 = on.torch.float32, on.torch.int32
+    torch, handle = _enter(logits, stream)
+    f32, i32 = torch.float32, torch.int32
     rows, vocab = logits.shape
     zp, zt, ld = _matrix("logits", logits)
-    out = [on.empty((rows,), f32) if tokens is not None else None,
-           on.empty((rows,), f32) if entropy else None, on.empty((rows, 2), f32)]
+    out = [_new(logits, (rows,), f32, stream) if tokens is not None else None,
+           _new(logits, (rows,), f32, stream) if entropy else None, _new(logits, (rows, 2), f32, stream)]
     ids = lps = None
     if top_k > 0:
-        ids, lps = on.empty((rows, top_k), i32), on.empty((rows, top_k), f32)
-    ws, wp, size = on.workspace(lib().mxq_vocab_workspace_size(rows, vocab, top_k))
+        ids, lps = _new(logits, (rows, top_k), i32, stream), _new(logits, (rows, top_k), f32, stream)
+    size = lib().mxq_vocab_workspace_size(rows, vocab, top_k)
+    ws = _new(logits, (size,), torch.uint8, stream) if size else None
     _check("mxq_token_logprobs", lib().mxq_token_logprobs(
         zp, zt, ld, rows, vocab, temperature, _vector("tokens", tokens, (rows,), logits, i32),
-        _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), top_k, _ptr(ids), _ptr(lps), wp, size, on.handle))
+        _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), top_k, _ptr(ids), _ptr(lps), _ptr(ws), size, handle))
     return out + [ids, lps] if top_k > 0 else out
 
 
@@ -624,23 +626,23 @@ def token_logprobs_backward(logits, tokens, stats, entropy=None, d_logprob=None,
                             temperature=1, out_dtype=None, out=None, stream=None):
     """mxq_token_logprobs_backward: the gradient of the logits, in their dtype
     unless out_dtype says otherwise, or in `out` (the logits themselves serve)."""
-    on = _On(logits, stream)
+    torch, handle = _enter(logits, stream)
     rows, vocab = logits.shape
-    o = on.empty((rows, vocab), out_dtype or logits.dtype) if out is None else out
+    o = _new(logits, (rows, vocab), out_dtype or logits.dtype, stream) if out is None else out
     zp, zt, ld = _matrix("logits", logits)
     op, ot, ldo = _matrix("out", o, logits)
     _check("mxq_token_logprobs_backward", lib().mxq_token_logprobs_backward(
         zp, zt, ld, rows, vocab, temperature,
-        _vector("tokens", tokens, (rows,), logits, on.torch.int32),
+        _vector("tokens", tokens, (rows,), logits, torch.int32),
         _vector("stats", stats, (rows, 2), logits), _vector("entropy", entropy, (rows,), logits),
         _vector("d_logprob", d_logprob, (rows,), logits),
-        _vector("d_entropy", d_entropy, (rows,), logits), op, ot, ldo, on.handle))
+        _vector("d_entropy", d_entropy, (rows,), logits), op, ot, ldo, handle))
     return o
 
 
-def _teacher_args(on, logits, ids, logprobs, weight, renormalize):
+def _teacher_args(logits, ids, logprobs, weight, renormalize):
     rows, top_k = logits.shape[0], ids.shape[-1]
-    return (_vector("teacher_ids", ids, (rows, top_k), logits, on.torch.int32),
+    return (_vector("teacher_ids", ids, (rows, top_k), logits, _torch.int32),
             _vector("teacher_logprobs", logprobs, (rows, top_k), logits), top_k,
             1 if renormalize else 0, _vector("weight", weight, (rows,), logits))
 
@@ -648,15 +650,16 @@ def _teacher_args(on, logits, ids, logprobs, weight, renormalize):
 def distill_forward(logits, teacher_ids, teacher_logprobs, weight=None, *, temperature=1,
                     renormalize=True, stream=None):
     """mxq_distill_forward: (loss, stats)."""
-    on = _On(logits, stream)
+    torch, handle = _enter(logits, stream)
     rows, vocab = logits.shape
     zp, zt, ld = _matrix("logits", logits)
-    loss, stats = on.empty((rows,), on.torch.float32), on.empty((rows, 2), on.torch.float32)
-    ws, wp, size = on.workspace(lib().mxq_vocab_workspace_size(rows, vocab, 0))
+    loss, stats = _new(logits, (rows,), torch.float32, stream), _new(logits, (rows, 2), torch.float32, stream)
+    size = lib().mxq_vocab_workspace_size(rows, vocab, 0)
+    ws = _new(logits, (size,), torch.uint8, stream) if size else None
     _check("mxq_distill_forward", lib().mxq_distill_forward(
         zp, zt, ld, rows, vocab, temperature,
-        *_teacher_args(on, logits, teacher_ids, teacher_logprobs, weight, renormalize),
-        _ptr(loss), _ptr(stats), wp, size, on.handle))
+        *_teacher_args(logits, teacher_ids, teacher_logprobs, weight, renormalize),
+        _ptr(loss), _ptr(stats), _ptr(ws), size, handle))
     return loss, stats
 
 
@@ -664,15 +667,15 @@ def distill_backward(logits, teacher_ids, teacher_logprobs, stats, weight=None, 
                      renormalize=True, out_dtype=None, out=None, stream=None):
     """mxq_distill_backward: the gradient of the logits, in their dtype unless
     out_dtype says otherwise, or in `out` (the logits themselves serve)."""
-    on = _On(logits, stream)
+    torch, handle = _enter(logits, stream)
     rows, vocab = logits.shape
-    o = on.empty((rows, vocab), out_dtype or logits.dtype) if out is None else out
+    o = _new(logits, (rows, vocab), out_dtype or logits.dtype, stream) if out is None else out
     zp, zt, ld = _matrix("logits", logits)
     op, ot, ldo = _matrix("out", o, logits)
     _check("mxq_distill_backward", lib().mxq_distill_backward(
         zp, zt, ld, rows, vocab, temperature,
-        *_teacher_args(on, logits, teacher_ids, teacher_logprobs, weight, renormalize),
-        _vector("stats", stats, (rows, 2), logits), op, ot, ldo, on.handle))
+        *_teacher_args(logits, teacher_ids, teacher_logprobs, weight, renormalize),
+        _vector("stats", stats, (rows, 2), logits), op, ot, ldo, handle))
     return o
 
 
@@ -680,15 +683,16 @@ def distill(logits, teacher_ids, teacher_logprobs, weight=None, *, temperature=1
             out_dtype=None, out=None, stream=None):
     """mxq_distill: (loss, gradient of the logits) in one pass; the gradient as
     in distill_backward."""
-    on = _On(logits, stream)
+    torch, handle = _enter(logits, stream)
     rows, vocab = logits.shape
-    o = on.empty((rows, vocab), out_dtype or logits.dtype) if out is None else out
+    o = _new(logits, (rows, vocab), out_dtype or logits.dtype, stream) if out is None else out
     zp, zt, ld = _matrix("logits", logits)
     op, ot, ldo = _matrix("out", o, logits)
-    loss = on.empty((rows,), on.torch.float32)
-    ws, wp, size = on.workspace(lib().mxq_vocab_workspace_size(rows, vocab, 0))
+    loss = _new(logits, (rows,), torch.float32, stream)
+    size = lib().mxq_vocab_workspace_size(rows, vocab, 0)
+    ws = _new(logits, (size,), torch.uint8, stream) if size else None
     _check("mxq_distill", lib().mxq_distill(
         zp, zt, ld, rows, vocab, temperature,
-        *_teacher_args(on, logits, teacher_ids, teacher_logprobs, weight, renormalize),
-        _ptr(loss), op, ot, ldo, wp, size, on.handle))
+        *_teacher_args(logits, teacher_ids, teacher_logprobs, weight, renormalize),
+        _ptr(loss), op, ot, ldo, _ptr(ws), size, handle))
     return loss, o
