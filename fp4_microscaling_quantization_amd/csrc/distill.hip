@@ -85,7 +85,7 @@ __device__ __forceinline__ Gradient distill_gradient(const Teacher &t, float w, 
 
 // a held stretch's gradient to o
 template <bool SLOPE, class T, class O, int NT, int NV>
-__device__ __forceinline__ void write_gradient(const Held<T, NT, NV> &held, O *o, int n,
+__device__ __forceinline__ void write_gradient(const Held<T, NT, NV> &held, O *o, int n, int lead,
                                                const Gradient &g, float log2)
 {
     constexpr int E = kElems<T>;
@@ -98,7 +98,7 @@ __device__ __forceinline__ void write_gradient(const Held<T, NT, NV> &held, O *o
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 f[j] = gradient_at<SLOPE>(f[j], g, log2);
-            held.put(o, i, n, f);
+            held.put(o, i, n, f, lead);
         }
     }
 }
@@ -193,15 +193,19 @@ k_distill_loss(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
             continue;
         }
         RowStats st = {-FLT_MAX, 0.0f, 0.0f};
+        int lead = lead_of<T, SHORT>(z);
+        const T *start = z - lead;
+        const int all = vocab + lead;
         for (int at = 0;;) {
-            const int n = min(vocab - at, H::kMost);
+            const int n = min(all - at, H::kMost);
             H held;
-            held.template load<SHORT, true>(z + at, n);
+            held.template load<SHORT, true>(start + at, n);
             float most[kGroups<T>];
-            absorb_held<false>(st, held, n, heat.log2, most);
-            if (vocab - at <= H::kMost)
+            absorb_held<false>(st, held, n, lead, heat.log2, most);
+            if (all - at <= H::kMost)
                 break;
             at += H::kMost;
+            lead = 0;
         }
         st = block_stats<kLossNT>(st, heat.log2, lds);
         if (threadIdx.x < 64) {
@@ -254,15 +258,17 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
         RowStats st = {-FLT_MAX, 0.0f, 0.0f};
         int at = 0, n = 0;
         float most[kGroups<T>];
+        const int lead = lead_of<T, SHORT>(z);
+        const T *start = z - lead;
         if constexpr (!SHORT) {
-            for (; vocab - at > H::kMost; at += H::kMost) {
-                held.template load<false, false>(z + at, H::kMost);
-                absorb_held<false>(st, held, H::kMost, heat.log2, most);
+            for (; vocab + lead - at > H::kMost; at += H::kMost) {
+                held.template load<false, false>(start + at, H::kMost);
+                absorb_held<false>(st, held, H::kMost, at == 0 ? lead : 0, heat.log2, most);
             }
         }
-        n = vocab - at;
-        held.template load<SHORT, true>(z + at, n);
-        absorb_held<false>(st, held, n, heat.log2, most);
+        n = vocab + lead - at;
+        held.template load<SHORT, true>(start + at, n);
+        absorb_held<false>(st, held, n, at == 0 ? lead : 0, heat.log2, most);
         const Teacher t = teacher_row(ta, r, vocab);
         const float zt = logit_at(z, t, 0, vocab);
         st = block_stats<NT>(st, heat.log2, lds);
@@ -274,12 +280,12 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
         } else {
             const Gradient g = distill_gradient(t, w, st, heat);
             for (;;) {
-                write_gradient<false>(held, o + at, n, g, heat.log2);
+                write_gradient<false>(held, o - lead + at, n, at == 0 ? lead : 0, g, heat.log2);
                 if (at == 0)
                     break;
                 at -= H::kMost;
                 n = H::kMost;
-                held.template load<SHORT, true>(z + at, n);
+                held.template load<SHORT, true>(start + at, n);
             }
             __syncthreads();
             if (threadIdx.x < 64 && !t.bad)
@@ -297,6 +303,23 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
 constexpr int kChunkNT = 256, kChunkNV = 4;
 template <class T> constexpr int kChunk = kChunkNT * kChunkNV * kElems<T>;
 
+// Chunk number `chunk` of the row at z: entries from `at` on, n of them with the `lead`
+// that lie before them; false: the row has none.  The chunks of a row that starts off a
+// 16-byte boundary are shifted, so the last may be a chunk more.
+template <class H, bool SHORT, class T>
+__device__ __forceinline__ bool chunk_of(const T *z, int vocab, int chunk, int &at, int &n,
+                                         int &lead)
+{
+    const int shift = lead_of<T, SHORT>(z);
+    const int64_t from = (int64_t)chunk * H::kMost;  // from the boundary
+    if (from >= (int64_t)vocab + shift)
+        return false;
+    lead = chunk == 0 ? shift : 0;
+    at = (int)(from + lead - shift);
+    n = (int)min((int64_t)vocab + shift - from, (int64_t)H::kMost);
+    return true;
+}
+
 // PARTS: the rows' statistics come from their parts, and the first chunk's workgroup
 // writes the loss; the gradient must not lie over the logits then.
 template <class T, class O, bool PARTS, bool SHORT>
@@ -308,21 +331,25 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
     using H = Held<T, kChunkNT, kChunkNV>;
     for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
         const int64_t r = b / chunks;
-        const int at = (int)(b - r * chunks) * H::kMost, n = min(vocab - at, H::kMost);
         const T *z = logits + r * ld;
         O *o = dlogits + r * ld_o;
+        // the row's entries from `at` on, or `lead` before them
+        int at, n, lead;
+        if (!chunk_of<H, SHORT>(z, vocab, (int)(b - r * chunks), at, n, lead))
+            continue;
         const float w = ta.weight ? ta.weight[r] : 1.0f;
         if (w == 0.0f) {
             if (PARTS && at == 0)
                 write_no_loss(loss, nullptr, r);
-            write_all<O, kChunkNT>(o + at, n, 0.0f);
+            write_all<O, kChunkNT>(o + at, n - lead, 0.0f);
             continue;
         }
         H held;
-        held.template load<SHORT, true>(z + at, n);
+        held.template load<SHORT, true>(z + at - lead, n);
         const Teacher t = teacher_row(ta, r, vocab);
-        const bool mine = t.id >= at && t.id < at + n;
-        float zt = logit_at(z, t, at, at + n);
+        const int end = at + n - lead;
+        const bool mine = t.id >= at && t.id < end;
+        const float zt = logit_at(z, t, at, end);
         RowStats st;
         if constexpr (PARTS) {
             st = part_stats(parts, rows, r, heat.log2);
@@ -332,17 +359,17 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
             st = {stats[2 * r], stats[2 * r + 1], 0.0f};
         }
         if (!counts(t, w)) {
-            write_all<O, kChunkNT>(o + at, n, 0.0f);
+            write_all<O, kChunkNT>(o + at, n - lead, 0.0f);
             continue;
         }
         // everything is read before anything is written over it
         held.again();
         __syncthreads();
         const Gradient g = distill_gradient(t, w, st, heat);
-        write_gradient<false>(held, o + at, n, g, heat.log2);
+        write_gradient<false>(held, o + at - lead, n, lead, g, heat.log2);
         __syncthreads();
         if (threadIdx.x < 64 && !t.bad && __any(mine))
-            write_ids(o, t, zt, at, at + n, g, w * heat.t, ta.top_k, heat.log2);
+            write_ids(o, t, zt, at, end, g, w * heat.t, ta.top_k, heat.log2);
     }
 }
 
@@ -356,11 +383,13 @@ k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks,
     constexpr float kLn2 = 0.69314718055994531f;
     for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
         const int64_t r = b / chunks;
-        const int at = (int)(b - r * chunks) * H::kMost, n = min(vocab - at, H::kMost);
         const T *z = logits + r * ld;
-        O *o = dlogits + r * ld_o + at;
+        O *o = dlogits + r * ld_o;
+        int at, n, lead;
+        if (!chunk_of<H, SHORT>(z, vocab, (int)(b - r * chunks), at, n, lead))
+            continue;
         H held;
-        held.template load<SHORT, true>(z + at, n);
+        held.template load<SHORT, true>(z + at - lead, n);
         const int token = d_logprob ? tokens[r] : -1;
         const float gl = token < 0 ? 0.0f : token >= vocab ? NAN : d_logprob[r] * heat.inv;
         const float gh = d_entropy ? d_entropy[r] * heat.inv : 0.0f;
@@ -374,15 +403,15 @@ k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks,
         } else if (token >= vocab) {
             g.k0 = NAN;
         }
-        const bool here = token >= at && token < at + n;
+        const bool here = token >= at && token < at + n - lead;
         float zt = here ? load_one(z + token) : 0.0f;
         asm volatile("" : "+v"(zt));
         held.again();
         __syncthreads();
-        write_gradient<true>(held, o, n, g, heat.log2);
+        write_gradient<true>(held, o + at - lead, n, lead, g, heat.log2);
         __syncthreads();
         if (here && threadIdx.x == 0)
-            o[token - at] = (O)(gl + gradient_at<true>(zt, g, heat.log2));
+            o[token] = (O)(gl + gradient_at<true>(zt, g, heat.log2));
     }
 }
 
@@ -396,7 +425,11 @@ mxq_status check_teacher(int64_t rows, const TeacherArgs &t)
 }
 
 // the chunks of a row, and the grid of a launch over them
-template <class T> int chunks_of(int64_t vocab) { return (int)((vocab + kChunk<T> - 1) / kChunk<T>); }
+// (bf16: a row may start up to 7 elements after the first one's boundary)
+template <class T> int chunks_of(int64_t vocab)
+{
+    return (int)((vocab + (sizeof(T) == 2 ? 7 : 0) + kChunk<T> - 1) / kChunk<T>);
+}
 unsigned chunk_grid(int64_t rows, int chunks)
 {
     return (unsigned)(rows < kMaxGrid / chunks ? rows * chunks : kMaxGrid);

@@ -118,7 +118,7 @@ __device__ __forceinline__ uint64_t list_of(uint64_t list, const uint64_t *keys,
 }
 
 // The first top_k alternatives of the held stretch (n logits, the first of them entry
-// `at` of the row) and of wave 0's list from before it, as wave 0's list.  most: the
+// `at` of the row, or `lead` before it) and of wave 0's list from before it, as wave 0's list.  most: the
 // thread's maxima of its groups of 16, top: its maximum over the row so far (the lowest
 // finite value where it has none).
 //
@@ -134,7 +134,7 @@ __device__ __forceinline__ uint64_t list_of(uint64_t list, const uint64_t *keys,
 // and reading them again with all lanes, 80 us, as the reads queue behind the other
 // workgroups' streams; ordering by counting larger keys with all waves, 106 us.
 template <class T>
-__device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, kNT, kHeld> &held, int at, int n,
+__device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, kNT, kHeld> &held, int at, int n, int lead,
                                              const float (&most)[kGroups<T>], float top, int top_k,
                                              Search &lds)
 {
@@ -174,7 +174,7 @@ __device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, kNT, kHeld> 
 #pragma unroll
             for (int k = i; k < i + G; ++k) {
                 float f[E];
-                held.get(k, n2, -INFINITY, f);
+                held.get(k, n2, -INFINITY, f, lead);
                 const int back = held.whole(k, n2) ? 0 : held.skip(k, n2);
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
@@ -253,17 +253,22 @@ __device__ __forceinline__ RowStats whole_part(const T *z, int first, int n, int
     using H = Held<T, kNT, kHeld>;
     RowStats st = {-FLT_MAX, 0.0f, 0.0f};
     list = 0;
+    int lead = lead_of<T, SHORT>(z);
+    z -= lead;
+    n += lead;
+    first -= lead;
     for (int at = 0;;) {
         const int here = min(n - at, H::kMost);
         H held;
         held.template load<SHORT, true>(z + at, here);
         float most[kGroups<T>];
-        absorb_held<true>(st, held, here, heat.log2, most);
+        absorb_held<true>(st, held, here, lead, heat.log2, most);
         if constexpr (TOP)
-            list = top_held(list, held, first + at, here, most, st.m, top_k, search);
+            list = top_held(list, held, first + at, here, lead, most, st.m, top_k, search);
         if (n - at <= H::kMost)
             break;
         at += H::kMost;
+        lead = 0;
     }
     return block_stats<kNT>(st, heat.log2, lds);
 }
@@ -360,7 +365,7 @@ using namespace mxq;
 
 extern "C" size_t mxq_vocab_workspace_size(int64_t rows, int64_t vocab, int32_t top_k)
 {
-    if (rows < 1 || vocab < 1 || vocab > INT32_MAX || top_k < 0 || top_k > MXQ_TOP_MAX)
+    if (rows < 1 || vocab < 1 || vocab > kMaxVocab || top_k < 0 || top_k > MXQ_TOP_MAX)
         return 0;
     const Parts p = parts_of(rows, vocab, top_k, nullptr);
     // and a row's m and s, joined

@@ -216,23 +216,25 @@ template <class T, int U> struct Unit {
 // gamma, and the sums over the rows of dy n and dy, stay in its registers, and dy
 // and x come from memory once for dx and the sums together.  The next row is
 // loaded before the present one is worked on.  With 1024 threads there are 128 registers:
-// gamma is in LDS then, and a row is loaded in its turn.
+// gamma is in LDS then, and a row is loaded in its turn, unless all is bf16 and dbeta is
+// not asked for (BIAS).
 // One barrier a row: the row's two sums go through alternating places in LDS.
 constexpr int kOwn = 16;  // columns of a thread
 template <class D, class X> constexpr int kUnit = sizeof(D) + sizeof(X) == 4 ? 8 : 4;
 
-template <class D, class X, int NT, int TR>
+template <class D, class X, int NT, int TR, bool BIAS>
 __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X *x, BwdArgs a)
 {
     constexpr int G = NT / TR, W = TR / 64, EL = kOwn, U = kUnit<D, X>, NU = EL / U;
-    constexpr bool kAhead = NT < 1024, kLdsGamma = NT == 1024;
+    constexpr bool kLdsGamma = NT == 1024;
+    constexpr bool kAhead = NT < 1024 || (!BIAS && sizeof(D) + sizeof(X) == 4);
     __shared__ float lds[2][2][NT / 64];
     __shared__ float sums[G > 1 ? EL * NT : 1];
     __shared__ gv4u gammas[kLdsGamma ? EL / 4 : 1][kLdsGamma ? TR : 1];
     const int t = threadIdx.x % TR, g = threadIdx.x / TR, wave = threadIdx.x / 64;
     const float inv = 1.0f / (float)a.cols;
 
-    float gamma[kLdsGamma ? 1 : EL], dg[EL], db[EL];
+    float gamma[kLdsGamma ? 1 : EL], dg[EL], db[BIAS ? EL : 1];
 #pragma unroll
     for (int e = 0; e < EL; ++e) {
         const int c = vec_start<U>((e / U * TR + t) * U, a.cols) + e % U;
@@ -241,7 +243,9 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
             gammas[e / 4][t][e % 4] = as_u(v);  // read by the same thread only
         else
             gamma[e] = v;
-        dg[e] = db[e] = 0.0f;
+        dg[e] = 0.0f;
+        if constexpr (BIAS)
+            db[e] = 0.0f;
     }
     const auto gamma_of = [&](int u, float (&out)[U]) {
 #pragma unroll
@@ -322,7 +326,8 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
                 su += w;
                 sun = fmaf(w, n, sun);
                 dg[e] = fmaf(d[j], n, dg[e]);
-                db[e] += d[j];
+                if constexpr (BIAS)
+                    db[e] += d[j];
             }
         }
         if (!a.dx)
@@ -373,17 +378,17 @@ __global__ void __launch_bounds__(NT, NT / 256) k_norm_bwd(const D *dy, const X 
     // part [2][workgroups][EL][TR]: the sums in the order of the threads
     const int64_t slots = EL * TR;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    for (int which = 0; which < (BIAS ? 2 : 1); ++which) {
         float *to = a.part + ((int64_t)which * gridDim.x + blockIdx.x) * slots;
         if constexpr (G == 1) {
 #pragma unroll
             for (int e = 0; e < EL; ++e)
-                to[e * TR + t] = which ? db[e] : dg[e];
+                to[e * TR + t] = which ? db[BIAS ? e : 0] : dg[e];
         } else {
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < EL; ++e)
-                sums[e * NT + threadIdx.x] = which ? db[e] : dg[e];
+                sums[e * NT + threadIdx.x] = which ? db[BIAS ? e : 0] : dg[e];
             __syncthreads();
             for (int s = threadIdx.x; s < EL * TR; s += NT) {
                 float v = 0.0f;
@@ -410,6 +415,7 @@ k_norm_sum(const float *part, int64_t groups, int tr, int unit, int cols, float 
     const int s = blockIdx.x * 64 + lane;
     const float *p = part + blockIdx.y * groups * slots + s;
     float v = 0.0f;
+#pragma unroll 16
     for (int64_t k = w; k < groups; k += 16)
         v += p[k * slots];
     lds[w][lane] = v;
@@ -542,16 +548,18 @@ BwdPlan plan_bwd(int64_t rows, int64_t cols)
 }
 
 template <class D, class X>
-void launch_bwd(const BwdPlan &p, const D *dy, const X *x, const BwdArgs &a, hipStream_t s)
+void launch_bwd(const BwdPlan &p, const D *dy, const X *x, const BwdArgs &a, bool bias,
+                hipStream_t s)
 {
-    const auto k = p.nt == 1024  ? k_norm_bwd<D, X, 1024, 1024>
-                   : p.nt == 512 ? (p.tr == 64    ? k_norm_bwd<D, X, 512, 64>
-                                    : p.tr == 128 ? k_norm_bwd<D, X, 512, 128>
-                                    : p.tr == 256 ? k_norm_bwd<D, X, 512, 256>
-                                                  : k_norm_bwd<D, X, 512, 512>)
-                                 : (p.tr == 64    ? k_norm_bwd<D, X, 256, 64>
-                                    : p.tr == 128 ? k_norm_bwd<D, X, 256, 128>
-                                                  : k_norm_bwd<D, X, 256, 256>);
+    const auto k = p.nt == 1024  ? (bias ? k_norm_bwd<D, X, 1024, 1024, true>
+                                         : k_norm_bwd<D, X, 1024, 1024, false>)
+                   : p.nt == 512 ? (p.tr == 64    ? k_norm_bwd<D, X, 512, 64, true>
+                                    : p.tr == 128 ? k_norm_bwd<D, X, 512, 128, true>
+                                    : p.tr == 256 ? k_norm_bwd<D, X, 512, 256, true>
+                                                  : k_norm_bwd<D, X, 512, 512, true>)
+                                 : (p.tr == 64    ? k_norm_bwd<D, X, 256, 64, true>
+                                    : p.tr == 128 ? k_norm_bwd<D, X, 256, 128, true>
+                                                  : k_norm_bwd<D, X, 256, 256, true>);
     hipLaunchKernelGGL(k, dim3((unsigned)p.groups), dim3(p.nt), 0, s, dy, x, a);
 }
 
@@ -646,7 +654,7 @@ extern "C" mxq_status mxq_norm_backward(int32_t kind, const void *dy, int32_t dy
                 const D *d = static_cast<const D *>(dy);
                 const X *xx = static_cast<const X *>(x);
                 if (p.nt) {
-                    launch_bwd(p, d, xx, a, s);
+                    launch_bwd(p, d, xx, a, dbeta != nullptr, s);
                     return;
                 }
                 // the sums first: dx may lie over dy or x

@@ -16,9 +16,8 @@ namespace mxq {
 typedef __bf16 bf16_t;
 
 // ---- 16-byte accesses ----------------------------------------------------------
-// Rows may start at any element (odd lengths, odd leading dimensions).  The
-// hardware takes 16-byte accesses at any address here, a wave's 1 KB then
-// touches one line more, so the same loads serve every alignment.
+// Rows may start at any element (odd lengths, odd leading dimensions); the hardware
+// takes 16-byte accesses at any address here.
 template <class T> constexpr int kElems = 16 / (int)sizeof(T);
 template <class T> struct Unaligned;
 template <> struct Unaligned<bf16_t> {
@@ -194,12 +193,13 @@ template <class T, int NT, int NV> struct Held {
             asm volatile("" : "+v"(v[i]));
     }
     __device__ __forceinline__ void get(int i, float (&f)[E]) const { unpack(v[i], f, (T *)nullptr); }
-    // what is not the thread's own is `none`
-    __device__ __forceinline__ void get(int i, int n, float none, float (&f)[E]) const
+    // What is not the thread's own is `none`; nor are the stretch's first `lead` < E
+    // elements (bf16 only).
+    __device__ __forceinline__ void get(int i, int n, float none, float (&f)[E], int lead = 0) const
     {
         get(i, f);
-        if (!whole(i, n)) {
-            const int d = skip(i, n);
+        if (!whole(i, n) || has_lead(i, lead)) {
+            const int d = first_own(i, n, lead);
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 f[j] = j >= d ? f[j] : none;
@@ -207,17 +207,38 @@ template <class T, int NT, int NV> struct Held {
     }
     // f as vector i of a stretch at o
     template <class O>
-    static __device__ __forceinline__ void put(O *o, int i, int n, const float (&f)[E])
+    static __device__ __forceinline__ void put(O *o, int i, int n, const float (&f)[E],
+                                               int lead = 0)
     {
-        if (whole(i, n)) {
+        if (whole(i, n) && !has_lead(i, lead)) {
             store_vec(lane_at<E>(o + i * NT * E), f);
         } else {
-            const int d = skip(i, n);
+            const int d = first_own(i, n, lead);
             if (d < E)
                 store_from(o + start(i, n), f, d);
         }
     }
+
+    static __device__ __forceinline__ bool has_lead(int i, int lead)
+    {
+        return sizeof(T) == 2 && i == 0 && lead > 0;
+    }
+    static __device__ __forceinline__ int first_own(int i, int n, int lead)
+    {
+        const int d = skip(i, n);
+        return has_lead(i, lead) && threadIdx.x == 0 ? lead : d;
+    }
 };
+
+// How many elements a row starts after a 16-byte boundary.  A bf16 row that starts in
+// the middle of a word reads a third slower (2048 x 50257 against x 50256: 47.9 and 37.6
+// us); its stretches then start at the boundary, and what lies before the row (within
+// the same 16 bytes, so in the same allocation) is not its own.  fp32 rows lose 3%
+// off the boundary and are left as they are, and so are rows shorter than a vector.
+template <class T, bool SHORT> __device__ __forceinline__ int lead_of(const T *row)
+{
+    return sizeof(T) == 2 && !SHORT ? (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 7) : 0;
+}
 
 // ---- reductions -----------------------------------------------------------------
 __device__ __forceinline__ float wave_sum(float v)

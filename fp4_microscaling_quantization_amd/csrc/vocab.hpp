@@ -79,10 +79,10 @@ __device__ __forceinline__ float absorb(RowStats &st, const float (&f)[N], float
 
 // The statistics of a held stretch of n elements into the threads' own states, 16
 // elements at a time: what a step costs beside its exponentials is shared by them.
-// most: the maxima of the thread's groups.
+// most: the maxima of the thread's groups.  lead: what of the stretch lies before the row.
 template <bool ENTROPY, class T, int NT>
 __device__ __forceinline__ void absorb_held(RowStats &st, const Held<T, NT, kHeld> &h, int n,
-                                            float log2, float (&most)[kGroups<T>])
+                                            int lead, float log2, float (&most)[kGroups<T>])
 {
     constexpr int E = kElems<T>, G = kGroup<T>;
     n = fresh(n);
@@ -94,7 +94,7 @@ __device__ __forceinline__ void absorb_held(RowStats &st, const Held<T, NT, kHel
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 float part[E];
-                h.get(i + g, n, -INFINITY, part);
+                h.get(i + g, n, -INFINITY, part, lead);
 #pragma unroll
                 for (int j = 0; j < E; ++j)
                     f[g * E + j] = part[j];
@@ -182,6 +182,7 @@ __device__ __forceinline__ RowStats part_stats(const Parts &p, int64_t rows, int
 // ---- the host's side -------------------------------------------------------------
 
 constexpr int64_t kMaxGrid = 1 << 20;  // workgroups of a launch over rows; more rows loop
+constexpr int64_t kMaxVocab = INT32_MAX - 63;  // an index and a shift to a boundary fit 32 bits
 
 inline unsigned row_grid(int64_t rows) { return (unsigned)(rows < kMaxGrid ? rows : kMaxGrid); }
 // Parts so that about 1024 workgroups of 256 threads run, four on a CU; a part has 4096
@@ -250,7 +251,7 @@ inline mxq_status check_logits(const void *logits, int32_t dtype, int64_t ld, in
 {
     if (!dtype_ok(dtype) || !(temperature >= FLT_MIN) || !(temperature < INFINITY))
         return MXQ_ERR_UNSUPPORTED;
-    if (rows < 0 || vocab < 1 || vocab > INT32_MAX || ld < vocab)
+    if (rows < 0 || vocab < 1 || vocab > kMaxVocab || ld < vocab)
         return MXQ_ERR_SHAPE;
     if (rows > 0 && !logits)
         return MXQ_ERR_NULL;

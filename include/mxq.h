@@ -388,8 +388,8 @@ size_t mxq_norm_backward_workspace_size(int64_t rows, int64_t cols);
  * alternatives, and where fewer than top_k are left, the ids are -1 and their
  * log q -inf.  A row with every logit masked has S = 0, entropy 0 and log q
  * -inf.  A row that holds a NaN or +inf has no distribution: its floating
- * outputs are NaN (stats: S), its ids -1.  1 <= vocab < 2^31, temperature finite
- * and > 0.
+ * outputs are NaN (stats: S), its ids -1.  1 <= vocab <= 2^31 - 64, temperature
+ * a positive normal number.
  * workspace: mxq_vocab_workspace_size(rows, vocab, top_k) bytes, 8-byte aligned
  * (may be NULL where that is 0). */
 #define MXQ_TOP_MAX 64
