@@ -176,6 +176,7 @@ template <class T, int NT, int NV> struct Held {
             for (int i = 1; i < NV; ++i)
                 v[i] = v[0];
         } else {
+            n = fresh(n);  // or the offsets of a loop's rows, all the same, are kept
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 // a uniform address and an unsigned offset: no 64-bit address per vector

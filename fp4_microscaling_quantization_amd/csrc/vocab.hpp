@@ -228,17 +228,17 @@ template <class F> void with_type(int32_t d, F f)
 }
 
 // f(integral constants: threads of a workgroup, whether the row is shorter than a
-// vector) for a row of n elements of T: the fewest threads that hold it, so that
-// short rows share a CU, and the widest beyond.
+// vector) for a row of n elements of T: the fewest threads that hold it from a boundary
+// on, so that short rows share a CU, and the widest beyond.
 template <class T, class F> void with_threads(int64_t n, F f)
 {
     constexpr int64_t one = 64 * kHeld * kElems<T>;  // what a wave holds
     constexpr std::false_type whole;
     if (n < kElems<T>)
         f(std::integral_constant<int, 256>(), std::true_type());
-    else if (n <= 4 * one)
+    else if (n + kElems<T> - 1 <= 4 * one)
         f(std::integral_constant<int, 256>(), whole);
-    else if (n <= 8 * one)
+    else if (n + kElems<T> - 1 <= 8 * one)
         f(std::integral_constant<int, 512>(), whole);
     else
         f(std::integral_constant<int, 1024>(), whole);
