@@ -177,14 +177,13 @@ __device__ __forceinline__ float logit_at(const T *z, const Teacher &t, int from
 }
 
 // One workgroup per row: loss and stats.
-constexpr int kLossNT = 256;
-template <class T, bool SHORT>
-__global__ void __launch_bounds__(kLossNT, 4)
+template <class T, int NT, bool SHORT>
+__global__ void __launch_bounds__(NT, 4)
 k_distill_loss(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, TeacherArgs ta,
                float *loss, float *stats)
 {
-    using H = Held<T, kLossNT, kHeld>;
-    __shared__ float lds[3 * kLossNT / 64];
+    using H = Held<T, NT, kHeld>;
+    __shared__ float lds[3 * NT / 64];
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *z = logits + r * ld;
         const float w = ta.weight ? ta.weight[r] : 1.0f;
@@ -200,14 +199,14 @@ k_distill_loss(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
             const int n = min(all - at, H::kMost);
             H held;
             held.template load<SHORT, true>(start + at, n);
-            float most[kGroups<T>];
-            absorb_held<false>(st, held, n, lead, heat.log2, most);
+            float most[kGroups<T>], half[2];
+            absorb_held<false>(st, held, n, lead, heat.log2, most, half);
             if (all - at <= H::kMost)
                 break;
             at += H::kMost;
             lead = 0;
         }
-        st = block_stats<kLossNT>(st, heat.log2, lds);
+        st = block_stats<NT>(st, heat.log2, lds);
         if (threadIdx.x < 64) {
             const Teacher t = teacher_row(ta, r, vocab);
             write_loss(loss, stats, r, t, logit_at(z, t, 0, vocab), w, vocab, st, heat);
@@ -261,13 +260,13 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
         H held;
         RowStats st = {-FLT_MAX, 0.0f, 0.0f};
         int at = 0, n = 0;
-        float most[kGroups<T>];
+        float most[kGroups<T>], half[2];
         const int lead = lead_of<T, SHORT>(z);
         const T *start = z - lead;
         if constexpr (LONG) {
             for (; vocab + lead - at > H::kMost; at += H::kMost) {
                 held.template load<false, false>(start + at, H::kMost);
-                absorb_held<false>(st, held, H::kMost, at == 0 ? lead : 0, heat.log2, most);
+                absorb_held<false>(st, held, H::kMost, at == 0 ? lead : 0, heat.log2, most, half);
                 if (at == 0) {
 #pragma unroll
                     for (int i = 0; i < kStaged; ++i)
@@ -277,7 +276,7 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
         }
         n = vocab + lead - at;
         held.template load<SHORT, true>(start + at, n);
-        absorb_held<false>(st, held, n, at == 0 ? lead : 0, heat.log2, most);
+        absorb_held<false>(st, held, n, at == 0 ? lead : 0, heat.log2, most, half);
         const Teacher t = teacher_row(ta, r, vocab);
         const float zt = logit_at(z, t, 0, vocab);
         st = block_stats<NT>(st, heat.log2, lds);
@@ -316,8 +315,8 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
 // A chunk of a row per workgroup: short enough that a few rows fill the chip, and
 // that several workgroups share a CU, so that one's loads run under another's
 // stores.
-constexpr int kChunkNT = 256, kChunkNV = 4;
-template <class T> constexpr int kChunk = kChunkNT * kChunkNV * kElems<T>;
+// Short rows, when there are many, are one chunk of a wave each.
+template <class T, int NT> using Chunk = Held<T, NT, NT == 64 ? 8 : 4>;
 
 // Chunk number `chunk` of the row at z: entries from `at` on, n of them with the `lead`
 // that lie before them; false: the row has none.  The chunks of a row that starts off a
@@ -338,13 +337,13 @@ __device__ __forceinline__ bool chunk_of(const T *z, int vocab, int chunk, int &
 
 // PARTS: the rows' statistics come from their parts, and the first chunk's workgroup
 // writes the loss; the gradient must not lie over the logits then.
-template <class T, class O, bool PARTS, bool SHORT>
-__global__ void __launch_bounds__(kChunkNT)
+template <class T, class O, int NT, bool PARTS, bool SHORT>
+__global__ void __launch_bounds__(NT)
 k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,
                  TeacherArgs ta, const float *stats, Parts parts, float *loss, O *dlogits,
                  int64_t ld_o)
 {
-    using H = Held<T, kChunkNT, kChunkNV>;
+    using H = Chunk<T, NT>;
     for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
         const int64_t r = b / chunks;
         const T *z = logits + r * ld;
@@ -357,7 +356,7 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
         if (w == 0.0f) {
             if (PARTS && at == 0)
                 write_no_loss(loss, nullptr, r);
-            write_all<O, kChunkNT>(o + at, n - lead, 0.0f);
+            write_all<O, NT>(o + at, n - lead, 0.0f);
             continue;
         }
         H held;
@@ -375,7 +374,7 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
             st = {stats[2 * r], stats[2 * r + 1], 0.0f};
         }
         if (!counts(t, w)) {
-            write_all<O, kChunkNT>(o + at, n - lead, 0.0f);
+            write_all<O, NT>(o + at, n - lead, 0.0f);
             continue;
         }
         // everything is read before anything is written over it
@@ -389,13 +388,13 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
     }
 }
 
-template <class T, class O, bool SHORT>
-__global__ void __launch_bounds__(kChunkNT)
+template <class T, class O, int NT, bool SHORT>
+__global__ void __launch_bounds__(NT)
 k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,
                const int32_t *tokens, const float *stats, const float *entropy,
                const float *d_logprob, const float *d_entropy, O *dlogits, int64_t ld_o)
 {
-    using H = Held<T, kChunkNT, kChunkNV>;
+    using H = Chunk<T, NT>;
     constexpr float kLn2 = 0.69314718055994531f;
     for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
         const int64_t r = b / chunks;
@@ -440,15 +439,20 @@ mxq_status check_teacher(int64_t rows, const TeacherArgs &t)
     return aligned4(t.ids) && aligned4(t.lps) && aligned4(t.weight) ? MXQ_OK : MXQ_ERR_ALIGN;
 }
 
-// the chunks of a row, and the grid of a launch over them
-// (bf16: a row may start up to 7 elements after the first one's boundary)
-template <class T> int chunks_of(int64_t vocab)
+// f(threads of a chunk's workgroup, chunks of a row, grid of a launch over them)
+template <class T, class F> void with_chunks(int64_t rows, int64_t vocab, F f)
 {
-    return (int)((vocab + (sizeof(T) == 2 ? 7 : 0) + kChunk<T> - 1) / kChunk<T>);
-}
-unsigned chunk_grid(int64_t rows, int chunks)
-{
-    return (unsigned)(rows < kMaxGrid / chunks ? rows * chunks : kMaxGrid);
+    // a row may start up to kElems - 1 elements after its first chunk's boundary
+    const int64_t most = vocab + kElems<T> - 1;
+    const auto go = [&](auto nt) {
+        constexpr int64_t size = Chunk<T, decltype(nt)::value>::kMost;
+        const int chunks = (int)((most + size - 1) / size);
+        f(nt, chunks, (unsigned)(rows < kMaxGrid / chunks ? rows * chunks : kMaxGrid));
+    };
+    if (vocab < kElems<T> || (most <= Chunk<T, 64>::kMost && rows >= kWaveRows))
+        go(std::integral_constant<int, 64>());
+    else
+        go(std::integral_constant<int, 256>());
 }
 
 // The logits of a call that was checked.
@@ -464,10 +468,13 @@ void launch_loss(const Logits &a, const TeacherArgs &ta, float *loss, float *sta
 {
     with_type(a.dtype, [&](auto *tt) {
         using T = std::remove_pointer_t<decltype(tt)>;
-        const auto k = a.vocab < kElems<T> ? k_distill_loss<T, true> : k_distill_loss<T, false>;
-        hipLaunchKernelGGL(k, dim3(row_grid(a.rows)), dim3(kLossNT), 0, s,
-                           static_cast<const T *>(a.z), a.ld, a.rows, (int)a.vocab, a.heat, ta,
-                           loss, stats);
+        with_threads<T, 256>(a.rows, a.vocab, [&](auto nt, auto is_short) {
+            constexpr int NT = decltype(nt)::value;
+            hipLaunchKernelGGL((k_distill_loss<T, NT, decltype(is_short)::value>),
+                               dim3(row_grid(a.rows)), dim3(NT), 0, s,
+                               static_cast<const T *>(a.z), a.ld, a.rows, (int)a.vocab, a.heat, ta,
+                               loss, stats);
+        });
     });
 }
 void launch_join(const Logits &a, const TeacherArgs &ta, const Parts &parts, float *loss,
@@ -487,7 +494,7 @@ void launch_rows(const Logits &a, const TeacherArgs &ta, float *loss, void *dlog
         with_type(o_dtype, [&](auto *ot) {
             using T = std::remove_pointer_t<decltype(tt)>;
             using O = std::remove_pointer_t<decltype(ot)>;
-            with_threads<T>(a.vocab, [&](auto nt, auto is_short) {
+            with_threads<T, 1024>(a.rows, a.vocab, [&](auto nt, auto is_short) {
                 constexpr int NT = decltype(nt)::value;
                 constexpr bool SHORT = decltype(is_short)::value;
                 auto k = k_distill_rows<T, O, NT, false, SHORT>;
@@ -511,13 +518,19 @@ void launch_chunks(const Logits &a, const TeacherArgs &ta, const float *stats, c
         with_type(o_dtype, [&](auto *ot) {
             using T = std::remove_pointer_t<decltype(tt)>;
             using O = std::remove_pointer_t<decltype(ot)>;
-            const int chunks = chunks_of<T>(a.vocab);
-            const auto k = parts.count > 1           ? k_distill_chunks<T, O, true, false>
-                           : a.vocab < kElems<T> ? k_distill_chunks<T, O, false, true>
-                                                     : k_distill_chunks<T, O, false, false>;
-            hipLaunchKernelGGL(k, dim3(chunk_grid(a.rows, chunks)), dim3(kChunkNT), 0, s,
-                               static_cast<const T *>(a.z), a.ld, a.rows, (int)a.vocab, chunks,
-                               a.heat, ta, stats, parts, loss, static_cast<O *>(dlogits), ld_o);
+            with_chunks<T>(a.rows, a.vocab, [&](auto nt, int chunks, unsigned grid) {
+                constexpr int NT = decltype(nt)::value;
+                auto k = k_distill_chunks<T, O, NT, false, false>;
+                if constexpr (NT == 64) {
+                    if (a.vocab < kElems<T>)
+                        k = k_distill_chunks<T, O, 64, false, true>;
+                } else if (parts.count > 1) {  // rows with parts are longer than a wave's chunk
+                    k = k_distill_chunks<T, O, NT, true, false>;
+                }
+                hipLaunchKernelGGL(k, dim3(grid), dim3(NT), 0, s, static_cast<const T *>(a.z),
+                                   a.ld, a.rows, (int)a.vocab, chunks, a.heat, ta, stats, parts,
+                                   loss, static_cast<O *>(dlogits), ld_o);
+            });
         });
     });
 }
@@ -548,12 +561,18 @@ extern "C" mxq_status mxq_token_logprobs_backward(
         with_type(dlogits_dtype, [&](auto *ot) {
             using T = std::remove_pointer_t<decltype(tt)>;
             using O = std::remove_pointer_t<decltype(ot)>;
-            const int chunks = chunks_of<T>(vocab);
-            const auto k = vocab < kElems<T> ? k_logprobs_bwd<T, O, true> : k_logprobs_bwd<T, O, false>;
-            hipLaunchKernelGGL(k, dim3(chunk_grid(rows, chunks)), dim3(kChunkNT), 0, s,
-                               static_cast<const T *>(logits), ld, rows, (int)vocab, chunks,
-                               heat_of(temperature), tokens, stats, entropy, d_logprob, d_entropy,
-                               static_cast<O *>(dlogits), ld_dlogits);
+            with_chunks<T>(rows, vocab, [&](auto nt, int chunks, unsigned grid) {
+                constexpr int NT = decltype(nt)::value;
+                auto k = k_logprobs_bwd<T, O, NT, false>;
+                if constexpr (NT == 64) {
+                    if (vocab < kElems<T>)
+                        k = k_logprobs_bwd<T, O, 64, true>;
+                }
+                hipLaunchKernelGGL(k, dim3(grid), dim3(NT), 0, s, static_cast<const T *>(logits),
+                                   ld, rows, (int)vocab, chunks, heat_of(temperature), tokens,
+                                   stats, entropy, d_logprob, d_entropy,
+                                   static_cast<O *>(dlogits), ld_dlogits);
+            });
         });
     });
     return launched();

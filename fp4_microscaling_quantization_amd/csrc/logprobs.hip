@@ -97,7 +97,6 @@ template <class K> __device__ __forceinline__ K wave_merge(K a, K b)
 }
 
 // What the search for the alternatives keeps in LDS.
-constexpr int kNT = 256;
 constexpr int kBuffer = 512, kPlaces = 128;
 struct Search {
     uint64_t buffer[kBuffer];
@@ -122,9 +121,10 @@ __device__ __forceinline__ uint64_t list_of(uint64_t list, const uint64_t *keys,
 // thread's maxima of its groups of 16, top: its maximum over the row so far (the lowest
 // finite value where it has none).
 //
-// A bound that top_k alternatives reach is known at once: the threads' maxima go
-// into 128 (64) places, the largest of each stays, and the top_k th of those is the
-// bound; twice as many places as alternatives keep it close (a random row has about
+// A bound that top_k alternatives reach is known at once: the threads' maxima go into
+// 128 (64) places, the largest of each stays, and the top_k th of those is the bound
+// (one wave: the places are its lanes' maxima, for over 32 alternatives of two halves
+// of what they hold); twice as many places as alternatives keep it close (a random row has about
 // 1.4 top_k logits that reach it).  Each wave goes over its registers, the groups whose
 // maximum reaches the bound, and puts what it finds into a buffer, which wave 0
 // sorts.  Where the buffer is too small (many equal logits, or the large ones all in a
@@ -133,9 +133,10 @@ __device__ __forceinline__ uint64_t list_of(uint64_t list, const uint64_t *keys,
 // Measured beside it (1501 x 50257 fp32, 64 alternatives, 73 us): listing the groups
 // and reading them again with all lanes, 80 us, as the reads queue behind the other
 // workgroups' streams; ordering by counting larger keys with all waves, 106 us.
-template <class T>
-__device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, kNT, kHeld> &held, int at, int n, int lead,
-                                             const float (&most)[kGroups<T>], float top, int top_k,
+template <class T, int NT>
+__device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, NT, kHeld> &held, int at, int n, int lead,
+                                             const float (&most)[kGroups<T>],
+                                             const float (&half)[2], float top, int top_k,
                                              Search &lds)
 {
     constexpr int E = kElems<T>, G = kGroup<T>;
@@ -144,19 +145,28 @@ __device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, kNT, kHeld> 
         const uint64_t k = (uint64_t)__shfl((unsigned long long)l, top_k - 1);
         return k > kLeastKey ? k : kLeastKey;
     };
-    if (threadIdx.x < kPlaces)
-        lds.most[threadIdx.x] = 0;
-    __syncthreads();
-    atomicMax(&lds.most[threadIdx.x & (places - 1)], order_of(top));
-    __syncthreads();
-    if (threadIdx.x < 64) {
-        uint32_t v = wave_sort(lds.most[lane]);
-        if (places == kPlaces)
-            v = wave_merge(v, wave_sort(lds.most[64 + lane]));
-        const uint64_t k = kth((uint64_t)v << 32), before = kth(list);
+    const auto start = [&](uint32_t sorted) {
+        const uint64_t k = kth((uint64_t)sorted << 32), before = kth(list);
         if (lane == 0) {
             lds.bound = k > before ? k : before;
             lds.count = 0;
+        }
+    };
+    if constexpr (NT == 64) {
+        // a wave has its row in one stretch
+        if (top_k > 32)
+            start(wave_merge(wave_sort(order_of(half[0])), wave_sort(order_of(half[1]))));
+        else
+            start(wave_sort(order_of(top)));
+    } else {
+        if (threadIdx.x < kPlaces)
+            lds.most[threadIdx.x] = 0;
+        __syncthreads();
+        atomicMax(&lds.most[threadIdx.x & (places - 1)], order_of(top));
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            const uint32_t v = wave_sort(lds.most[lane]);
+            start(places == kPlaces ? wave_merge(v, wave_sort(lds.most[64 + lane])) : v);
         }
     }
     __syncthreads();
@@ -179,7 +189,7 @@ __device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, kNT, kHeld> 
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
                     if (f[j] >= least) {
-                        const uint64_t key = key_of(f[j], mine - back + k * kNT * E + j);
+                        const uint64_t key = key_of(f[j], mine - back + k * NT * E + j);
                         if (key >= bound) {
                             const int to = atomicAdd(&lds.count, 1);
                             if (to < kBuffer)
@@ -245,12 +255,12 @@ __device__ __forceinline__ void write_row(const LogprobOut &out, const T *z, int
 
 // The statistics of n logits at z, entry `first` of their row the first, and wave 0's list
 // of their alternatives.
-template <class T, bool TOP, bool SHORT, class S>
+template <class T, int NT, bool TOP, bool SHORT, class S>
 __device__ __forceinline__ RowStats whole_part(const T *z, int first, int n, int top_k,
                                                const Heat &heat, float *lds, S &search,
                                                uint64_t &list)
 {
-    using H = Held<T, kNT, kHeld>;
+    using H = Held<T, NT, kHeld>;
     RowStats st = {-FLT_MAX, 0.0f, 0.0f};
     list = 0;
     int lead = lead_of<T, SHORT>(z);
@@ -261,29 +271,29 @@ __device__ __forceinline__ RowStats whole_part(const T *z, int first, int n, int
         const int here = min(n - at, H::kMost);
         H held;
         held.template load<SHORT, true>(z + at, here);
-        float most[kGroups<T>];
-        absorb_held<true>(st, held, here, lead, heat.log2, most);
+        float most[kGroups<T>], half[2];
+        absorb_held<true>(st, held, here, lead, heat.log2, most, half);
         if constexpr (TOP)
-            list = top_held(list, held, first + at, here, lead, most, st.m, top_k, search);
+            list = top_held(list, held, first + at, here, lead, most, half, st.m, top_k, search);
         if (n - at <= H::kMost)
             break;
         at += H::kMost;
         lead = 0;
     }
-    return block_stats<kNT>(st, heat.log2, lds);
+    return block_stats<NT>(st, heat.log2, lds);
 }
 
-template <class T, bool TOP, bool SHORT>
-__global__ void __launch_bounds__(kNT, 4)
+template <class T, int NT, bool TOP, bool SHORT>
+__global__ void __launch_bounds__(NT, 4)
 k_logprobs(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, LogprobOut out)
 {
-    __shared__ float lds[3 * kNT / 64];
+    __shared__ float lds[3 * NT / 64];
     __shared__ typename std::conditional<TOP, Search, char>::type search;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *z = logits + r * ld;
         uint64_t list;
         const RowStats st =
-            whole_part<T, TOP, SHORT>(z, 0, vocab, out.top_k, heat, lds, search, list);
+            whole_part<T, NT, TOP, SHORT>(z, 0, vocab, out.top_k, heat, lds, search, list);
         if (threadIdx.x < 64)
             write_row(out, z, r, vocab, st, list, heat);
         __syncthreads();
@@ -291,16 +301,17 @@ k_logprobs(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, Logp
 }
 
 // one workgroup per part of a row
+constexpr int kPartNT = 256;
 template <class T, bool TOP>
-__global__ void __launch_bounds__(kNT, 4)
+__global__ void __launch_bounds__(kPartNT, 4)
 k_parts(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, int top_k, Parts parts)
 {
-    __shared__ float lds[3 * kNT / 64];
+    __shared__ float lds[3 * kPartNT / 64];
     __shared__ typename std::conditional<TOP, Search, char>::type search;
     const int64_t b = blockIdx.x, r = b / parts.count;
     const int at = (int)(b - r * parts.count) * parts.length;
     uint64_t list;
-    const RowStats st = whole_part<T, TOP, false>(logits + r * ld + at, at,
+    const RowStats st = whole_part<T, kPartNT, TOP, false>(logits + r * ld + at, at,
                                                   min(vocab - at, parts.length), top_k, heat, lds,
                                                   search, list);
     if (threadIdx.x == 0) {
@@ -355,7 +366,7 @@ void mxq::launch_parts(const void *logits, int32_t dtype, int64_t ld, int64_t ro
     with_type(dtype, [&](auto *tt) {
         using T = std::remove_pointer_t<decltype(tt)>;
         hipLaunchKernelGGL((top_k > 0 ? k_parts<T, true> : k_parts<T, false>),
-                           dim3((unsigned)(rows * parts.count)), dim3(kNT), 0, s,
+                           dim3((unsigned)(rows * parts.count)), dim3(kPartNT), 0, s,
                            static_cast<const T *>(logits), ld, rows, (int)vocab, heat, top_k,
                            parts);
     });
@@ -408,12 +419,14 @@ extern "C" mxq_status mxq_token_logprobs(const void *logits, int32_t dtype, int6
                                heat_of(temperature), out, parts);
             return;
         }
-        const bool is_short = vocab < kElems<T>;
-        const auto k = top_k > 0 ? (is_short ? k_logprobs<T, true, true> : k_logprobs<T, true, false>)
-                                 : (is_short ? k_logprobs<T, false, true> : k_logprobs<T, false, false>);
-        hipLaunchKernelGGL(k, dim3(row_grid(rows)), dim3(kNT), 0, s,
-                           static_cast<const T *>(logits), ld, rows, (int)vocab,
-                           heat_of(temperature), out);
+        with_threads<T, 256>(rows, vocab, [&](auto nt, auto is_short) {
+            constexpr int NT = decltype(nt)::value;
+            constexpr bool SHORT = decltype(is_short)::value;
+            const auto k = top_k > 0 ? k_logprobs<T, NT, true, SHORT> : k_logprobs<T, NT, false, SHORT>;
+            hipLaunchKernelGGL(k, dim3(row_grid(rows)), dim3(NT), 0, s,
+                               static_cast<const T *>(logits), ld, rows, (int)vocab,
+                               heat_of(temperature), out);
+        });
     });
     return launched();
 }

@@ -47,16 +47,19 @@ __device__ __forceinline__ void move_to(RowStats &st, float to, float log2)
     st.m = to;
 }
 
-// takes the values in, and returns their maximum
+// takes the values in; half: the maxima of their two halves
 template <bool ENTROPY, int N>
-__device__ __forceinline__ float absorb(RowStats &st, const float (&f)[N], float log2)
+__device__ __forceinline__ void absorb(RowStats &st, const float (&f)[N], float log2,
+                                       float (&half)[2])
 {
-    float m = f[0];
+    half[0] = f[0];
+    half[1] = f[N / 2];
 #pragma unroll
-    for (int j = 1; j < N; ++j)
-        m = fmaxf(m, f[j]);
-    const float most = m;
-    m = fmaxf(st.m, m);
+    for (int j = 1; j < N / 2; ++j) {
+        half[0] = fmaxf(half[0], f[j]);
+        half[1] = fmaxf(half[1], f[N / 2 + j]);
+    }
+    const float m = fmaxf(st.m, fmaxf(half[0], half[1]));
     const float d = fmaxf((st.m - m) * log2, kFloorLog2);
     const float sc = __builtin_amdgcn_exp2f(d);
     if (ENTROPY)
@@ -74,18 +77,20 @@ __device__ __forceinline__ float absorb(RowStats &st, const float (&f)[N], float
     if (ENTROPY)
         st.a += a;
     st.m = m;
-    return most;
 }
 
 // The statistics of a held stretch of n elements into the threads' own states, 16
 // elements at a time: what a step costs beside its exponentials is shared by them.
-// most: the maxima of the thread's groups.  lead: what of the stretch lies before the row.
+// most: the maxima of the thread's groups, half: those of the groups' first and second
+// halves.  lead: what of the stretch lies before the row.
 template <bool ENTROPY, class T, int NT>
 __device__ __forceinline__ void absorb_held(RowStats &st, const Held<T, NT, kHeld> &h, int n,
-                                            int lead, float log2, float (&most)[kGroups<T>])
+                                            int lead, float log2, float (&most)[kGroups<T>],
+                                            float (&half)[2])
 {
     constexpr int E = kElems<T>, G = kGroup<T>;
     n = fresh(n);
+    half[0] = half[1] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kHeld; i += G) {
         most[i / G] = -INFINITY;
@@ -99,7 +104,11 @@ __device__ __forceinline__ void absorb_held(RowStats &st, const Held<T, NT, kHel
                 for (int j = 0; j < E; ++j)
                     f[g * E + j] = part[j];
             }
-            most[i / G] = absorb<ENTROPY>(st, f, log2);
+            float h2[2];
+            absorb<ENTROPY>(st, f, log2, h2);
+            most[i / G] = fmaxf(h2[0], h2[1]);
+            half[0] = fmaxf(half[0], h2[0]);
+            half[1] = fmaxf(half[1], h2[1]);
         }
     }
 }
@@ -228,20 +237,25 @@ template <class F> void with_type(int32_t d, F f)
 }
 
 // f(integral constants: threads of a workgroup, whether the row is shorter than a
-// vector) for a row of n elements of T: the fewest threads that hold it from a boundary
-// on, so that short rows share a CU, and the widest beyond.
-template <class T, class F> void with_threads(int64_t n, F f)
+// vector) for rows of n elements of T: the fewest threads that hold a row from a
+// boundary on, so that rows share a CU, up to `MOST`.  A wave a row only where there are
+// enough rows to fill the chip with waves.
+constexpr int64_t kWaveRows = 2048;
+template <class T, int MOST, class F> void with_threads(int64_t rows, int64_t n, F f)
 {
     constexpr int64_t one = 64 * kHeld * kElems<T>;  // what a wave holds
     constexpr std::false_type whole;
+    const int64_t most = n + kElems<T> - 1;
     if (n < kElems<T>)
-        f(std::integral_constant<int, 256>(), std::true_type());
-    else if (n + kElems<T> - 1 <= 4 * one)
+        f(std::integral_constant<int, 64>(), std::true_type());
+    else if (most <= one && rows >= kWaveRows)
+        f(std::integral_constant<int, 64>(), whole);
+    else if (MOST == 256 || most <= 4 * one)
         f(std::integral_constant<int, 256>(), whole);
-    else if (n + kElems<T> - 1 <= 8 * one)
-        f(std::integral_constant<int, 512>(), whole);
+    else if (most <= 8 * one)
+        f(std::integral_constant<int, MOST < 512 ? 256 : 512>(), whole);
     else
-        f(std::integral_constant<int, 1024>(), whole);
+        f(std::integral_constant<int, MOST>(), whole);
 }
 
 // The checks that every call over a vocabulary shares: the logits and the
