@@ -21,9 +21,8 @@ struct TeacherArgs {
     const float *weight;
 };
 
-// A row's teacher, one alternative per lane, the same in every wave: its id (-1:
-// absent), log p and p (0 where absent); their sum; whether an id is beyond the
-// vocabulary; whether some p is not 0.
+// A row's teacher, one alternative per lane: its id (-1: absent), log p and p (0 where
+// absent); their sum; whether an id is beyond the vocabulary; whether some p is not 0.
 struct Teacher {
     int id;
     float p, logp, sum;
@@ -46,6 +45,29 @@ __device__ __forceinline__ Teacher teacher_row(const TeacherArgs &a, int64_t r, 
     t.sum = wave_sum(t.p);
     t.used = __any(!(t.p == 0.0f));
     return t;
+}
+// The same for a workgroup: wave 0 has it, the others what the whole row needs, after a
+// barrier, through share_teacher.
+struct Shared {
+    float sum;
+    int bad, used;
+};
+__device__ __forceinline__ Teacher wave0_teacher(const TeacherArgs &a, int64_t r, int vocab,
+                                                 Shared &lds)
+{
+    Teacher t = {-1, 0.0f, 0.0f, 0.0f, false, false};
+    if (threadIdx.x < 64) {
+        t = teacher_row(a, r, vocab);
+        if (threadIdx.x == 0)
+            lds = {t.sum, t.bad, t.used};
+    }
+    return t;
+}
+__device__ __forceinline__ void share_teacher(Teacher &t, const Shared &lds)
+{
+    t.sum = lds.sum;
+    t.bad = lds.bad;
+    t.used = lds.used;
 }
 __device__ __forceinline__ bool counts(const Teacher &t, float w)
 {
@@ -127,15 +149,17 @@ template <class O, int NT> __device__ __forceinline__ void write_all(O *o, int n
 // writes the same value.  Called by one wave, after a barrier.
 template <class O>
 __device__ __forceinline__ void write_ids(O *o, const Teacher &t, float zt, int from, int to,
-                                          const Gradient &g, float wt, int top_k, float log2)
+                                          const Gradient &g, float wt, float log2)
 {
+    const bool mine = t.id >= from && t.id < to;
     float p = 0.0f;
-    for (int j = 0; j < top_k; ++j) {
-        const int id = __shfl(t.id, j);
-        const float pj = __shfl(t.p, j);
+    for (uint64_t left = __ballot(mine); left; left &= left - 1) {
+        const int j = __ffsll((unsigned long long)left) - 1;
+        const int id = __builtin_amdgcn_readlane(t.id, j);
+        const float pj = as_f((uint32_t)__builtin_amdgcn_readlane((int)as_u(t.p), j));
         p += id == t.id ? pj : 0.0f;
     }
-    if (t.id >= from && t.id < to)
+    if (mine)
         o[t.id] = (O)fmaf(-wt, p, gradient_at<false>(zt, g, log2));
 }
 
@@ -248,6 +272,7 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
     using H = Held<T, NT, kHeld>;
     __shared__ float lds[3 * NT / 64];
     __shared__ gv4u staged[LONG ? kStaged : 1][LONG ? NT : 1];
+    __shared__ Shared teacher;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *z = logits + r * ld;
         O *o = dlogits + r * ld_o;
@@ -277,9 +302,10 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
         n = vocab + lead - at;
         held.template load<SHORT, true>(start + at, n);
         absorb_held<false>(st, held, n, at == 0 ? lead : 0, heat.log2, most, half);
-        const Teacher t = teacher_row(ta, r, vocab);
+        Teacher t = wave0_teacher(ta, r, vocab, teacher);
         const float zt = logit_at(z, t, 0, vocab);
         st = block_stats<NT>(st, heat.log2, lds);
+        share_teacher(t, teacher);
         held.again();
         if (threadIdx.x < 64)
             write_loss(loss, nullptr, r, t, zt, w, vocab, st, heat);
@@ -304,7 +330,7 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
             }
             __syncthreads();
             if (threadIdx.x < 64 && !t.bad)
-                write_ids(o, t, zt, 0, vocab, g, w * heat.t, ta.top_k, heat.log2);
+                write_ids(o, t, zt, 0, vocab, g, w * heat.t, heat.log2);
         }
         __syncthreads();
     }
@@ -344,6 +370,7 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
                  int64_t ld_o)
 {
     using H = Chunk<T, NT>;
+    __shared__ Shared teacher;
     for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
         const int64_t r = b / chunks;
         const T *z = logits + r * ld;
@@ -361,9 +388,8 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
         }
         H held;
         held.template load<SHORT, true>(z + at - lead, n);
-        const Teacher t = teacher_row(ta, r, vocab);
+        Teacher t = wave0_teacher(ta, r, vocab, teacher);
         const int end = at + n - lead;
-        const bool mine = t.id >= at && t.id < end;
         const float zt = logit_at(z, t, at, end);
         RowStats st;
         if constexpr (PARTS) {
@@ -373,18 +399,20 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
         } else {
             st = {stats[2 * r], stats[2 * r + 1], 0.0f};
         }
-        if (!counts(t, w)) {
-            write_all<O, NT>(o + at, n - lead, 0.0f);
-            continue;
-        }
         // everything is read before anything is written over it
         held.again();
         __syncthreads();
+        share_teacher(t, teacher);
+        if (!counts(t, w)) {
+            write_all<O, NT>(o + at, n - lead, 0.0f);
+            __syncthreads();
+            continue;
+        }
         const Gradient g = distill_gradient(t, w, st, heat);
         write_gradient<false>(held, o + at - lead, n, lead, g, heat.log2);
         __syncthreads();
-        if (threadIdx.x < 64 && !t.bad && __any(mine))
-            write_ids(o, t, zt, at, end, g, w * heat.t, ta.top_k, heat.log2);
+        if (threadIdx.x < 64 && !t.bad)
+            write_ids(o, t, zt, at, end, g, w * heat.t, heat.log2);
     }
 }
 
