@@ -283,6 +283,10 @@ __device__ __forceinline__ RowStats whole_part(const T *z, int first, int n, int
     return block_stats<NT>(st, heat.log2, lds);
 }
 
+// One workgroup per row, four of 256 threads on a CU.  2048 x 128256 bf16 (525 MB): 86 us
+// without alternatives (6.1 TB/s, memory), 114 us with 32 and 128 us with 64, where the
+// search's latency and the vector arithmetic (12 instructions an element, VALUBusy 73%)
+// come on top.  1501 x 50257 fp32: 49 us without (6.2 TB/s), 72 us with 64.
 template <class T, int NT, bool TOP, bool SHORT>
 __global__ void __launch_bounds__(NT, 4)
 k_logprobs(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, LogprobOut out)
@@ -300,7 +304,8 @@ k_logprobs(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, Logp
     }
 }
 
-// one workgroup per part of a row
+// One workgroup per part of a row: 4 x 128256 bf16 with 20 alternatives 7.9 us, and 5.2 us
+// for the join.
 constexpr int kPartNT = 256;
 template <class T, bool TOP>
 __global__ void __launch_bounds__(kPartNT, 4)

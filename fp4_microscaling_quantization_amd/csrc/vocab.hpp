@@ -241,7 +241,8 @@ template <class F> void with_type(int32_t d, F f)
 // f(integral constants: threads of a workgroup, whether the row is shorter than a
 // vector) for rows of n elements of T: the fewest threads that hold a row from a
 // boundary on, so that rows share a CU, up to `MOST`.  A wave a row only where there are
-// enough rows to fill the chip with waves.
+// enough rows to fill the chip with waves: log probabilities of 8192 x 1000 bf16 17 us
+// against 48 with 256 threads, but of 1024 x 8000 14.3 against 12.7.
 constexpr int64_t kWaveRows = 2048;
 template <class T, int MOST, class F> void with_threads(int64_t rows, int64_t n, F f)
 {
