@@ -31,11 +31,12 @@ struct Teacher {
 };
 __device__ __forceinline__ Teacher teacher_row(const TeacherArgs &a, int64_t r, int vocab)
 {
-    const int lane = threadIdx.x & 63;
+    unsigned lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // or both addresses are kept for the loop over rows, and spilled
     Teacher t;
-    t.id = lane < a.top_k ? a.ids[r * a.top_k + lane] : -1;
+    t.id = lane < (unsigned)a.top_k ? (a.ids + r * a.top_k)[lane] : -1;
     t.bad = __any(t.id >= vocab);
-    t.logp = t.id >= 0 ? a.lps[r * a.top_k + lane] : -INFINITY;
+    t.logp = t.id >= 0 ? (a.lps + r * a.top_k)[lane] : -INFINITY;
     if (a.renormalize) {
         const float m = base_of(wave_max(t.logp));
         const float s = wave_sum(expf(t.logp - m));
@@ -52,6 +53,10 @@ __device__ __forceinline__ Teacher teacher_row(const TeacherArgs &a, int64_t r, 
 struct Shared {
     float sum;
     int bad, used;
+    // what wave 0 writes after the row's gradient, and where (-1: nothing): here and not in
+    // registers, which k_distill_rows has none to spare of
+    int id[64];
+    float dz[64];
 };
 __device__ __forceinline__ Teacher wave0_teacher(const TeacherArgs &a, int64_t r, int vocab,
                                                  Shared &lds)
@@ -59,8 +64,11 @@ __device__ __forceinline__ Teacher wave0_teacher(const TeacherArgs &a, int64_t r
     Teacher t = {-1, 0.0f, 0.0f, 0.0f, false, false};
     if (threadIdx.x < 64) {
         t = teacher_row(a, r, vocab);
-        if (threadIdx.x == 0)
-            lds = {t.sum, t.bad, t.used};
+        if (threadIdx.x == 0) {
+            lds.sum = t.sum;
+            lds.bad = t.bad;
+            lds.used = t.used;
+        }
     }
     return t;
 }
@@ -130,6 +138,7 @@ __device__ __forceinline__ void write_gradient(const Held<T, NT, NV> &held, O *o
 template <class O, int NT> __device__ __forceinline__ void write_all(O *o, int n, float value)
 {
     constexpr int E = kElems<O>;
+    asm volatile("" : "+v"(value));  // or its vector is kept for the loop over rows, and spilled
     float f[E];
 #pragma unroll
     for (int j = 0; j < E; ++j)
@@ -144,13 +153,11 @@ template <class O, int NT> __device__ __forceinline__ void write_all(O *o, int n
     }
 }
 
-// The entries of the teacher's ids in [from, to) once more, with their p: zt is the
-// logit there, loaded before the row was written (the gradient may lie over the
-// logits).  An id that comes twice: each of its lanes has the sum of both p and
-// writes the same value.  Called by one wave, after a barrier.
-template <class O>
-__device__ __forceinline__ void write_ids(O *o, const Teacher &t, float zt, int from, int to,
-                                          const Gradient &g, float wt, float log2)
+// The gradient at the lane's id, if that is in [from, to), with its p: zt is the logit
+// there, loaded before the row was written (the gradient may lie over the logits).  An
+// id that comes twice: each of its lanes has the sum of both p, and so the same value.
+__device__ __forceinline__ float id_gradient(const Teacher &t, float zt, int from, int to,
+                                             const Gradient &g, float wt, float log2)
 {
     const bool mine = t.id >= from && t.id < to;
     float p = 0.0f;
@@ -160,8 +167,16 @@ __device__ __forceinline__ void write_ids(O *o, const Teacher &t, float zt, int 
         const float pj = as_f((uint32_t)__builtin_amdgcn_readlane((int)as_u(t.p), j));
         p += id == t.id ? pj : 0.0f;
     }
-    if (mine)
-        o[t.id] = (O)fmaf(-wt, p, gradient_at<false>(zt, g, log2));
+    return fmaf(-wt, p, gradient_at<false>(zt, g, log2));
+}
+// The entries of these ids once more; called by one wave, after a barrier.
+template <class O>
+__device__ __forceinline__ void write_ids(O *o, const Teacher &t, float zt, int from, int to,
+                                          const Gradient &g, float wt, float log2)
+{
+    const float dz = id_gradient(t, zt, from, to, g, wt, log2);
+    if (t.id >= from && t.id < to)
+        o[t.id] = (O)dz;
 }
 
 // ---- whole rows ----------------------------------------------------------------------
@@ -263,9 +278,10 @@ k_distill_join(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
 // One workgroup per row: loss and dlogits.  The row is held; of a row longer than the
 // registers hold (LONG), half of the first stretch stays in LDS, and what is left before
 // the last stretch is read again for the gradient, from the last-level cache.  Bound by
-// memory: 4096 x 128256 fp32 to bf16 with a tenth of the rows ignored, 2.94 GB, 548 us
-// (5.4 TB/s; before the LDS the second reading cost 53 us more), and 4096 x 32000 fp32 to
-// bf16, which is held whole, 150 us (5.2 TB/s).
+// memory: 4096 x 128256 fp32 to bf16 with a tenth of the rows ignored, 2.94 GB, 531 us
+// (5.5 TB/s; the LDS saved 53 us of the second reading), and 4096 x 32000 fp32 to bf16,
+// which is held whole, 134 us (5.9 TB/s).  Registers are short: 8 spilled ones, 32 bytes
+// a thread that nothing read again, cost 17 us.
 constexpr int kStaged = 8;  // vectors a thread has in LDS: 128 KB of the CU's 160
 template <class T, class O, int NT, bool LONG, bool SHORT>
 __global__ void __launch_bounds__(NT, 4)
@@ -316,6 +332,10 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
             write_all<O, NT>(o, vocab, 0.0f);
         } else {
             const Gradient g = distill_gradient(t, w, st, heat);
+            if (threadIdx.x < 64) {
+                teacher.id[threadIdx.x] = t.bad ? -1 : t.id;
+                teacher.dz[threadIdx.x] = id_gradient(t, zt, 0, vocab, g, w * heat.t, heat.log2);
+            }
             for (;;) {
                 write_gradient<false>(held, o - lead + at, n, at == 0 ? lead : 0, g, heat.log2);
                 if (!LONG || at == 0)
@@ -332,8 +352,8 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
                 }
             }
             __syncthreads();
-            if (threadIdx.x < 64 && !t.bad)
-                write_ids(o, t, zt, 0, vocab, g, w * heat.t, heat.log2);
+            if (threadIdx.x < 64 && teacher.id[threadIdx.x] >= 0)
+                o[teacher.id[threadIdx.x]] = (O)teacher.dz[threadIdx.x];
         }
         __syncthreads();
     }
