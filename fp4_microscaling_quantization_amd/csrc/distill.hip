@@ -440,7 +440,9 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
     }
 }
 
-// The gradient of log probabilities and entropy: 1024 x 32000 fp32 to bf16 38 us, 5.2 TB/s.
+// The gradient of log probabilities and entropy: 1024 x 32000 fp32 to bf16 38 us, 5.2 TB/s
+// (chunks of twice the vectors 36, but 26 against 23 from bf16, and 3.9 against 3.3 for 4
+// rows of 128256).
 template <class T, class O, int NT, bool SHORT>
 __global__ void __launch_bounds__(NT)
 k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,
