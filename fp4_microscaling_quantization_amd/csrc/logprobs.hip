@@ -132,7 +132,10 @@ __device__ __forceinline__ uint64_t list_of(uint64_t list, const uint64_t *keys,
 // again, until it is not: every key of the buffer is an alternative of the row.
 // Measured beside it (1501 x 50257 fp32, 64 alternatives, 73 us): listing the groups
 // and reading them again with all lanes, 80 us, as the reads queue behind the other
-// workgroups' streams; ordering by counting larger keys with all waves, 106 us.
+// workgroups' streams; ordering by counting larger keys with all waves, 106 us.  Keys of
+// several stretches sorted at once, 2% faster here and 3% on 2048 x 128256 bf16, but 2 to
+// 4% slower on rows of eight stretches (1024 x 128256 fp32), where the list's own last key
+// is the closer bound.
 template <class T, int NT>
 __device__ __forceinline__ uint64_t top_held(uint64_t list, Held<T, NT, kHeld> &held, int at, int n, int lead,
                                              const float (&most)[kGroups<T>],
@@ -283,10 +286,10 @@ __device__ __forceinline__ RowStats whole_part(const T *z, int first, int n, int
     return block_stats<NT>(st, heat.log2, lds);
 }
 
-// One workgroup per row, four of 256 threads on a CU.  2048 x 128256 bf16 (525 MB): 86 us
-// without alternatives (6.1 TB/s, memory), 114 us with 32 and 128 us with 64, where the
-// search's latency and the vector arithmetic (12 instructions an element, VALUBusy 73%)
-// come on top.  1501 x 50257 fp32: 49 us without (6.2 TB/s), 72 us with 64.
+// One workgroup per row, four of 256 threads on a CU.  2048 x 128256 bf16 (525 MB): 86 to
+// 95 us without alternatives (5.5 to 6.1 TB/s, memory), 114 us with 32 and 128 us with 64,
+// where the search's latency and the vector arithmetic (12 instructions an element,
+// VALUBusy 73%) come on top.  1501 x 50257 fp32: 49 us without (6.2 TB/s), 72 us with 64.
 template <class T, int NT, bool TOP, bool SHORT>
 __global__ void __launch_bounds__(NT, 4)
 k_logprobs(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, LogprobOut out)
