@@ -514,7 +514,7 @@ template <class T, class F> void with_chunks(int64_t rows, int64_t vocab, F f)
 // twice and are two launches, which pays for a few long rows: 4 x 128256 fp32 7.6 us
 // against 17.0 whole, 48 rows 17.3 against 19.3, 64 rows 21.6 against 19.4; of bf16 64
 // rows 15.4 against 17.4, 96 rows 20.5 against 17.8 (the one limit in bytes is a little
-// late for bf16); rows of up to 128 KB gain nothing, 16 x 50257 bf16 9.8 against 10.3.
+// late for bf16); rows of up to 128 KB gain little, 16 x 50257 bf16 9.8 against 10.3.
 bool whole_rows(int64_t rows, int64_t vocab, int32_t dtype)
 {
     const int64_t row = vocab * (dtype == MXQ_OUT_F32 ? 4 : 2);
