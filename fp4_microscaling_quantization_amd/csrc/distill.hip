@@ -88,7 +88,8 @@ __device__ __forceinline__ float row_loss(const Teacher &t, float zt, bool have,
 {
     const float term = have && t.p != 0.0f ? t.p * (t.logp - log_q(zt, st, h)) : 0.0f;
     const float sum = wave_sum(term);
-    return t.bad ? NAN : w * (h.t * h.t * sum);
+    // temperature^2 need not be an fp32 number: the sum is of the order of 1 / T or 1 / T^2
+    return t.bad ? NAN : w * (h.t * (h.t * sum));
 }
 
 // ---- gradients -----------------------------------------------------------------------
