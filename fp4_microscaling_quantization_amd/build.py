@@ -4,6 +4,10 @@ hipcc compiles every source under csrc/ into one shared library next to this
 file.  Flags: -O3, no floating-point contraction (each rounding in the
 quantizer is the single IEEE operation written), and packed-fp32
 instructions disabled.
+
+Beside it stands libmxq_loop.so, for the tests: the same library with launches
+over rows of at most LOOP_GRID workgroups, so that few rows make every
+workgroup take several in turn.
 """
 import glob
 import os
@@ -12,6 +16,9 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmxq.so")
+LOOP_LIB = os.path.join(HERE, "libmxq_loop.so")
+LOOP_GRID = 5
+LOOP_SOURCES = ("norm.hip", "logprobs.hip", "distill.hip")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
@@ -29,24 +36,34 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
               "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"),
               "-Wall", "-Wno-unused-function", "-Werror=inline-asm"]
     procs = []
-    objs = []
-    for src in sources():
-        obj = os.path.join(objdir, os.path.basename(src) + ".o")
-        objs.append(obj)
+
+    def compile_to(src, obj, flags):
         lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmd = [HIPCC] + common + lang + ["-c", src, "-o", obj]
+        cmd = [HIPCC] + common + flags + lang + ["-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd))
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         if len(procs) >= jobs:
             _wait(procs.pop(0))
+        return obj
+
+    def link(objs, lib):
+        cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950"] + objs + ["-o", lib + ".tmp"]
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.run(cmd, check=True)
+        os.replace(lib + ".tmp", lib)
+
+    objs, loop_objs = [], []
+    for src in sources():
+        name = os.path.basename(src)
+        objs.append(compile_to(src, os.path.join(objdir, name + ".o"), []))
+        loop_objs.append(compile_to(src, os.path.join(objdir, name + ".loop.o"),
+                                    [f"-DMXQ_ROW_GRID={LOOP_GRID}"]) if name in LOOP_SOURCES else objs[-1])
     for p in procs:
         _wait(p)
-    link = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950"] + objs + ["-o", LIB + ".tmp"]
-    if verbose:
-        print(" ".join(link))
-    subprocess.run(link, check=True)
-    os.replace(LIB + ".tmp", LIB)
+    link(objs, LIB)
+    link(loop_objs, LOOP_LIB)
     return LIB
 
 

@@ -10,8 +10,6 @@ namespace mxq {
 
 namespace {
 
-constexpr int64_t kMaxGrid = 1 << 20;  // workgroups of a launch over rows; more rows loop
-
 // ---- forward -------------------------------------------------------------------------
 
 struct FwdArgs {

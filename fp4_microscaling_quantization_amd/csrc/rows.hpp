@@ -15,6 +15,13 @@ namespace mxq {
 
 typedef __bf16 bf16_t;
 
+// Workgroups of a launch over rows; more rows loop.  (The tests have a build in which a
+// handful of rows do.)
+#ifndef MXQ_ROW_GRID
+#define MXQ_ROW_GRID (1 << 20)
+#endif
+constexpr int64_t kMaxGrid = MXQ_ROW_GRID;
+
 // ---- 16-byte accesses ----------------------------------------------------------
 // Rows may start at any element (odd lengths, odd leading dimensions); the hardware
 // takes 16-byte accesses at any address here.

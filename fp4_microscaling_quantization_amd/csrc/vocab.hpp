@@ -190,7 +190,6 @@ __device__ __forceinline__ RowStats part_stats(const Parts &p, int64_t rows, int
 
 // ---- the host's side -------------------------------------------------------------
 
-constexpr int64_t kMaxGrid = 1 << 20;  // workgroups of a launch over rows; more rows loop
 constexpr int64_t kMaxVocab = INT32_MAX - 63;  // an index and a shift to a boundary fit 32 bits
 
 inline unsigned row_grid(int64_t rows) { return (unsigned)(rows < kMaxGrid ? rows : kMaxGrid); }
