@@ -408,8 +408,9 @@ size_t mxq_vocab_workspace_size(int64_t rows, int64_t vocab, int32_t top_k);
  *   dz_v = (d_logprob (1[v = token] - q_v) - d_entropy q_v (log q_v + entropy)) / temperature
  * into dlogits (all vocab columns of every row; may be logits itself, same
  * dtype and leading dimension).  Token < 0: d_logprob counts as 0;
- * token >= vocab: the row is NaN.  Masked logits have q = 0, rows without a
- * distribution are NaN. */
+ * token >= vocab: the row is NaN.  Masked logits have q = 0, so a row with every
+ * logit masked has the gradient d_logprob / temperature at its token and 0
+ * elsewhere.  Rows without a distribution are NaN. */
 mxq_status mxq_token_logprobs_backward(const void *logits, int32_t dtype, int64_t ld,
                                        int64_t rows, int64_t vocab, float temperature,
                                        const int32_t *tokens, const float *stats,
@@ -430,7 +431,8 @@ mxq_status mxq_token_logprobs_backward(const void *logits, int32_t dtype, int64_
  * A row with w = 0, or without a present alternative of p > 0, has loss 0 and
  * gradient 0 whatever else it holds; an id >= vocab makes its row NaN.  An id may
  * come twice.  Where a p > 0 meets a masked logit, the loss is +inf and the
- * gradient finite.
+ * gradient finite; with every logit masked (q = 0) the gradient is
+ * -w temperature p at the ids and 0 elsewhere.
  *   mxq_distill_forward:  loss and stats (as mxq_token_logprobs writes them;
  *                         rows of w = 0 get (0, 1)).
  *   mxq_distill_backward: dlogits from stats; w then is the gradient of the
