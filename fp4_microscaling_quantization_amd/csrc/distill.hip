@@ -281,8 +281,11 @@ k_distill_join(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
 // the last stretch is read again for the gradient, from the last-level cache.  Bound by
 // memory: 4096 x 128256 fp32 to bf16 with a tenth of the rows ignored, 2.94 GB, 531 us
 // (5.5 TB/s; the LDS saved 53 us of the second reading), and 4096 x 32000 fp32 to bf16,
-// which is held whole, 134 us (5.9 TB/s).  Registers are short: 8 spilled ones, 32 bytes
-// a thread that nothing read again, cost 17 us.
+// which is held whole, 134 us (5.9 TB/s).  bf16 to fp32 2048 x 128256 497 us (3.2 TB/s; to bf16
+// 196 us, 5.4): a store's lanes, 16 bytes each, are 32 bytes apart.  Registers are short: 8 spilled
+// ones, 32 bytes a thread that nothing read again, cost 17 us of the first case.  The fp32 forms
+// spill none now; those of bf16 rows longer than the registers hold, which have `lead` on top,
+// still spill 13 (to bf16) and 4 (to fp32).
 constexpr int kStaged = 8;  // vectors a thread has in LDS: 128 KB of the CU's 160
 template <class T, class O, int NT, bool LONG, bool SHORT>
 __global__ void __launch_bounds__(NT, 4)
@@ -365,7 +368,8 @@ k_distill_rows(const T *logits, int64_t ld, int64_t rows, int vocab, Heat heat, 
 // A chunk of a row per workgroup: short enough that a few rows fill the chip, and
 // that several workgroups share a CU, so that one's loads run under another's
 // stores.  4096 x 128256 fp32 to bf16 505 us, 6.2 TB/s; 2048 x 50257 bf16 85 us, 4.9 TB/s
-// (chunks of twice the vectors 538 and 93 us, of half 590 and 101 us).
+// (chunks of twice the vectors 538 and 93 us, of half 590 and 101 us).  bf16 to fp32 2048 x
+// 128256 349 us, 4.5 TB/s, for the stores' sake (k_distill_rows).
 // Short rows, when there are many, are one chunk of a wave each.
 template <class T, int NT> using Chunk = Held<T, NT, NT == 64 ? 8 : 4>;
 
@@ -443,7 +447,7 @@ k_distill_chunks(const T *logits, int64_t ld, int64_t rows, int vocab, int chunk
 
 // The gradient of log probabilities and entropy: 1024 x 32000 fp32 to bf16 38 us, 5.2 TB/s
 // (chunks of twice the vectors 36, but 26 against 23 from bf16, and 3.9 against 3.3 for 4
-// rows of 128256).
+// rows of 128256).  bf16 to fp32 2048 x 128256 456 us, 3.5 TB/s; to bf16 187 us, 5.6.
 template <class T, class O, int NT, bool SHORT>
 __global__ void __launch_bounds__(NT)
 k_logprobs_bwd(const T *logits, int64_t ld, int64_t rows, int vocab, int chunks, Heat heat,

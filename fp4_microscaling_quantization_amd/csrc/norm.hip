@@ -66,7 +66,9 @@ template <int NT> __device__ __forceinline__ float row_sum(float v, float *lds)
 // differences from the mean, a second pass over registers: mean(x^2) - mu^2 loses
 // what the two have in common.  Two rows share the loads of gamma and beta, which for
 // a bf16 row are four times its own bytes (from L2: the row streams through L1).  Bound by
-// memory: 8192 x 4096 bf16 24 us, 5.7 TB/s (34 us with one row a wave).
+// memory: 8192 x 4096 bf16 24 us, 5.7 TB/s (34 us with one row a wave).  Rows that a wave does
+// not hold have nobody to share with: 8192 x 8192 bf16 71 us, 3.8 TB/s.  fp32 from bf16, where a
+// store's lanes are 32 bytes apart: 8192 x 4096 66 us, 3.1 TB/s (fp32 from fp32 54 us, 5.0).
 template <class X, int NT, int NV, int R, bool LONG, bool SHORT>
 __global__ void __launch_bounds__(NT) k_norm_fwd(const X *x, FwdArgs a)
 {
@@ -433,8 +435,11 @@ k_norm_sum(const float *part, int64_t groups, int tr, int unit, int cols, float 
 }
 
 // ---- backward of other rows ------------------------------------------------------------
-// Wider rows, and rows shorter than a vector.  dx a row at a time, the sums a column at a
-// time; dy and x are read once for each.
+// Rows wider than 1024 threads hold, and rows shorter than a vector.  dx a row at a time, from
+// two reads of dy and x, the sums a column at a time, from another; one element a thread.  They
+// are right and no more: layer norm of 2048 x 16392 bf16 187 us (1.1 TB/s of what has to move)
+// where 2048 x 16384 in the kernel above takes 54, fp32 286 and 86 us; 262144 x 7 bf16 520 us,
+// 262144 x 8 162 us.
 
 constexpr int kWideNT = 256;
 
@@ -526,7 +531,9 @@ constexpr int64_t kTwoRows = 4096;
 // the workgroups are those that fill the chip once.  512 threads: 2048 x 4096 bf16 20.6 us,
 // with 256 threads, so twice the workgroups and sums to add up, 24.5; 300 rows 14.0 and 14.6;
 // 515 x 200 fp32 7.8 and 8.7.  Where that makes no more than kFewGroups workgroups, 256
-// threads: 64 x 1024 bf16 7.2 us against 9.1, 40 x 4096 fp32 7.2 against 8.2.
+// threads: 64 x 1024 bf16 7.2 us against 9.1, 40 x 4096 fp32 7.2 against 8.2.  Rows that take more
+// than 512 threads: 1024, against the kernels for other rows (RMS, bf16) 16 x 8200 8.4 us and 21,
+// 2048 x 9216 34 and 128, 8192 x 16384 144 and 598.
 struct BwdPlan {
     int nt, tr;      // nt 0: the kernels for other rows
     int64_t groups;  // workgroups (other rows: strips), each with a set of sums
@@ -598,7 +605,11 @@ extern "C" mxq_status mxq_norm_forward(int32_t kind, const void *x, int32_t x_dt
         const X *xx = static_cast<const X *>(x);
         hipStream_t s = static_cast<hipStream_t>(stream);
         constexpr int64_t one = 64 * 8 * kElems<X>;  // what a wave holds
-        // a wave per row while it holds the row: no barrier; two rows when there are enough
+        // The fewest threads that hold the row, a wave (no barrier) if one does; two rows a wave
+        // when there are enough.  64 and 256 threads, bf16: 3000 x 4096 11.4 and 16.6 us, 8192 x
+        // 2048 13.4 and 24.4, but 16 x 4096 5.4 and 3.8, 1024 x 4096 7.9 and 6.1.  256 and 1024:
+        // 1024 x 8192 8.6 and 17.2, 8192 x 8192 71 and 121, 8192 x 16384 142 and 158, but 16 x
+        // 16384 6.8 and 5.5.
         const bool two = cols >= kElems<X> && cols <= one && rows >= kTwoRows;
         const auto k = cols < kElems<X>   ? k_norm_fwd<X, 64, 8, 1, false, true>
                        : two              ? k_norm_fwd<X, 64, 8, 2, false, false>

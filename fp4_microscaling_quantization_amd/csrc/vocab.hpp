@@ -241,7 +241,13 @@ template <class F> void with_type(int32_t d, F f)
 // vector) for rows of n elements of T: the fewest threads that hold a row from a
 // boundary on, so that rows share a CU, up to `MOST`.  A wave a row only where there are
 // enough rows to fill the chip with waves: log probabilities of 8192 x 1000 bf16 17 us
-// against 48 with 256 threads, but of 1024 x 8000 14.3 against 12.7.
+// against 48 with 256 threads, but of 1024 x 8000 14.3 against 12.7.  With 256, 512 and 1024
+// threads where 256 hold the row: distillation of 4096 x 32000 bf16 102, 105 and 142 us, 4096 x
+// 16000 59, 76 and 121, 600 x 32000 21.0, 22.0 and 27.6, but 64 x 32000 10.7, 8.8 and 9.3; with 512
+// and 1024, 4096 x 64000 186 and 213.  What is only read takes 256 at any length (MOST): log
+// probabilities with 32 alternatives of 2048 x 128256 bf16 114, 122 and 136 us, 2048 x 32000 37, 44
+// and 71, without 25.5, 26.5 and 43, but 2048 x 64000 without 48.5, 44 and 61, 64 x 32000 with 32
+// 12.6, 10.4 and 9.6.
 constexpr int64_t kWaveRows = 2048;
 template <class T, int MOST, class F> void with_threads(int64_t rows, int64_t n, F f)
 {
