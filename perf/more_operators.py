@@ -21,29 +21,29 @@ SIZE = {"f32": 4, "bf16": 2}
 def listed():
     return [
         # the loss of one token after a prompt: latency, and a weight of 64 MB to read
-        dict(name="head loss, one token", op="ce", rows=1, hidden=1024, vocab=32000, ignored=0.0, temperature=1.0),
+        dict(name="head loss: one token", op="ce", rows=1, hidden=1024, vocab=32000, ignored=0.0, temperature=1.0),
         # scoring a few continuations with a large vocabulary: one read of the weight
-        dict(name="head loss, a few tokens", op="ce", rows=24, hidden=4096, vocab=128256, ignored=0.0, temperature=1.0),
+        dict(name="head loss: a few tokens", op="ce", rows=24, hidden=4096, vocab=128256, ignored=0.0, temperature=1.0),
         # evaluation of a text in windows of odd length, with a vocabulary that is no multiple of anything
-        dict(name="head loss, odd", op="ce", rows=1501, hidden=1600, vocab=50257, ignored=0.0, temperature=1.0),
+        dict(name="head loss: odd", op="ce", rows=1501, hidden=1600, vocab=50257, ignored=0.0, temperature=1.0),
         # a training step of 8192 tokens, a tenth of them padding
-        dict(name="head loss, step", op="ce", rows=8192, hidden=4096, vocab=128256, ignored=0.1, temperature=1.0),
+        dict(name="head loss: step", op="ce", rows=8192, hidden=4096, vocab=128256, ignored=0.1, temperature=1.0),
         # the backward pass of a few tokens: the weight and its gradient are all there is to move
-        dict(name="head loss backward, a few tokens", op="ce_bwd", rows=16, hidden=4096, vocab=32003, ignored=0.0, temperature=1.0),
+        dict(name="head loss backward: a few tokens", op="ce_bwd", rows=16, hidden=4096, vocab=32003, ignored=0.0, temperature=1.0),
         # a micro-batch with an odd vocabulary, at a temperature
-        dict(name="head loss backward, odd", op="ce_bwd", rows=1501, hidden=1600, vocab=50257, ignored=0.1, temperature=0.7),
+        dict(name="head loss backward: odd", op="ce_bwd", rows=1501, hidden=1600, vocab=50257, ignored=0.1, temperature=0.7),
         # fine-tuning on answers: more than half of the tokens are prompt and do not count
-        dict(name="head loss backward, answers", op="ce_bwd", rows=4096, hidden=4096, vocab=32000, ignored=0.6, temperature=1.0),
+        dict(name="head loss backward: answers", op="ce_bwd", rows=4096, hidden=4096, vocab=32000, ignored=0.6, temperature=1.0),
         # the backward pass of the training step
-        dict(name="head loss backward, step", op="ce_bwd", rows=8192, hidden=4096, vocab=128256, ignored=0.1, temperature=1.0),
+        dict(name="head loss backward: step", op="ce_bwd", rows=8192, hidden=4096, vocab=128256, ignored=0.1, temperature=1.0),
         # the norm of one small layer's gradients, for a log: latency
-        dict(name="gradient norm, small layer", op="norm", layers=1, hidden=512, inner=1024, vocab=0, g="f32"),
+        dict(name="gradient norm: small layer", op="norm", layers=1, hidden=512, inner=1024, vocab=0, g="f32"),
         # a shard of a large model's gradients in bf16, whose squares are summed over the ranks next
-        dict(name="gradient norm, shard", op="norm", layers=4, hidden=4096, inner=14336, vocab=32000, g="bf16"),
+        dict(name="gradient norm: shard", op="norm", layers=4, hidden=4096, inner=14336, vocab=32000, g="bf16"),
         # some hundred tensors of odd sizes, adapters and norms among them, clipped into fp32
-        dict(name="clipping, odd tensors", op="clip", count=700, largest=200003, g="bf16", out="f32", over=True),
+        dict(name="clipping: odd tensors", op="clip", count=700, largest=200003, g="bf16", out="f32", over=True),
         # the fp32 gradients of layers and output layer, clipped into the bf16 that the optimizer reads
-        dict(name="clipping, layers and head", op="clip", layers=4, hidden=4096, inner=14336, vocab=128256, g="f32", out="bf16", over=True),
+        dict(name="clipping: layers and head", op="clip", layers=4, hidden=4096, inner=14336, vocab=128256, g="f32", out="bf16", over=True),
     ]
 
 
