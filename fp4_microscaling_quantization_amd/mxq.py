@@ -28,7 +28,8 @@ SYMBOLS = ("mxq_quantize", "mxq_quantize_batch", "mxq_dequantize", "mxq_wgrad_ge
            "mxq_bias_stats_workspace_size", "mxq_bias_stats_noalloc", "mxq_bucket_ratio", "mxq_round_to_grid", "mxq_rht_sign_mask", "mxq_rotate",
            "mxq_norm_forward", "mxq_norm_backward", "mxq_norm_backward_workspace_size", "mxq_token_logprobs",
            "mxq_token_logprobs_backward", "mxq_vocab_workspace_size", "mxq_distill_forward",
-           "mxq_distill_backward", "mxq_distill", "mxq_status_string", "mxq_abi_version")
+           "mxq_distill_backward", "mxq_distill", "mxq_linear_ce_forward", "mxq_linear_ce_forward_workspace_size",
+           "mxq_linear_ce_backward", "mxq_linear_ce_backward_workspace_size", "mxq_status_string", "mxq_abi_version")
 
 
 class QConfig(C.Structure):
@@ -108,6 +109,12 @@ def lib() -> C.CDLL:
         L.mxq_distill_forward.argtypes = logits + teacher + [P, P, P, sz, P]
         L.mxq_distill_backward.argtypes = logits + teacher + [P, P, i32, i64, P]
         L.mxq_distill.argtypes = logits + teacher + [P, P, i32, i64, P, sz, P]
+        head = [P, i64, P, i64, i64, i64, i64, f32, P, P]
+        L.mxq_linear_ce_forward.argtypes = head + [P, P, P, sz, P]
+        L.mxq_linear_ce_backward.argtypes = head + [P, P, i64, P, i64, P, sz, P]
+        for name in ("mxq_linear_ce_forward_workspace_size", "mxq_linear_ce_backward_workspace_size"):
+            getattr(L, name).argtypes = [i64, i64, i64]
+            getattr(L, name).restype = sz
         L.mxq_status_string.argtypes = [i32]
         L.mxq_status_string.restype = C.c_char_p
         L.mxq_abi_version.restype = i32
@@ -115,7 +122,7 @@ def lib() -> C.CDLL:
                      "mxq_bias_stats", "mxq_bias_stats_noalloc", "mxq_round_to_grid", "mxq_rotate",
                      "mxq_norm_forward", "mxq_norm_backward", "mxq_token_logprobs",
                      "mxq_token_logprobs_backward", "mxq_distill_forward", "mxq_distill_backward",
-                     "mxq_distill"):
+                     "mxq_distill", "mxq_linear_ce_forward", "mxq_linear_ce_backward"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -696,3 +703,55 @@ def distill(logits, teacher_ids, teacher_logprobs, weight=None, *, temperature=1
         *_teacher_args(logits, teacher_ids, teacher_logprobs, weight, renormalize),
         _ptr(loss), op, ot, ldo, _ptr(ws), size, handle))
     return loss, o
+
+
+# ---- the ends of a training step ---------------------------------------------
+
+def _bf16(name, t, shape, like):
+    """(address, leading dimension) of a 2-D bf16 tensor of this shape whose rows are contiguous."""
+    p, code, ld = _matrix(name, t)
+    if code != OUT_BF16 or tuple(t.shape) != tuple(shape) or t.device != like.device:
+        raise ValueError(f"{name}: bfloat16 of shape {tuple(shape)} on {like.device} expected, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return p, ld
+
+
+def linear_ce_forward(x, w, targets, weight=None, *, temperature=1, stream=None):
+    """mxq_linear_ce_forward: (loss, stats) of the output layer with weight w
+    [vocab, hidden] on the hidden states x [rows, hidden]."""
+    torch, handle = _enter(x, stream)
+    (rows, hidden), vocab = x.shape, w.shape[0]
+    xp, ldx = _bf16("x", x, (rows, hidden), x)
+    wp, ldw = _bf16("w", w, (vocab, hidden), x)
+    loss, stats = _new(x, (rows,), torch.float32, stream), _new(x, (rows, 2), torch.float32, stream)
+    size = lib().mxq_linear_ce_forward_workspace_size(rows, hidden, vocab)
+    ws = _new(x, (size,), torch.uint8, stream) if size else None
+    _check("mxq_linear_ce_forward", lib().mxq_linear_ce_forward(
+        xp, ldx, wp, ldw, rows, hidden, vocab, temperature,
+        _vector("targets", targets, (rows,), x, torch.int32), _vector("weight", weight, (rows,), x),
+        _ptr(loss), _ptr(stats), _ptr(ws), size, handle))
+    return loss, stats
+
+
+def linear_ce_backward(x, w, targets, stats, weight=None, *, temperature=1, dx=True, dw=True, stream=None):
+    """mxq_linear_ce_backward: (dx, dw), new tensors for True, None for False; a
+    tensor takes the gradient itself."""
+    torch, handle = _enter(x, stream)
+    (rows, hidden), vocab = x.shape, w.shape[0]
+    xp, ldx = _bf16("x", x, (rows, hidden), x)
+    wp, ldw = _bf16("w", w, (vocab, hidden), x)
+
+    def gradient(name, given, shape):
+        if given is False or given is None:
+            return None, None, 0
+        t = _new(x, shape, torch.bfloat16, stream) if given is True else given
+        return (t, *_bf16(name, t, shape, x))
+    dx, dxp, lddx = gradient("dx", dx, (rows, hidden))
+    dw, dwp, lddw = gradient("dw", dw, (vocab, hidden))
+    size = lib().mxq_linear_ce_backward_workspace_size(rows, hidden, vocab)
+    ws = _new(x, (size,), torch.uint8, stream) if size else None
+    _check("mxq_linear_ce_backward", lib().mxq_linear_ce_backward(
+        xp, ldx, wp, ldw, rows, hidden, vocab, temperature,
+        _vector("targets", targets, (rows,), x, torch.int32), _vector("weight", weight, (rows,), x),
+        _vector("stats", stats, (rows, 2), x), dxp, lddx, dwp, lddw, _ptr(ws), size, handle))
+    return dx, dw

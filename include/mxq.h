@@ -456,6 +456,46 @@ mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t ro
                        const float *weight, float *loss, void *dlogits, int32_t dlogits_dtype,
                        int64_t ld_dlogits, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- the ends of a training step --------------------------------------------
+ * Softmax cross entropy of an output layer from its hidden states and weight,
+ * a piece of the vocabulary at a time: the logits z = x w^T are never kept, so
+ * the workspaces do not grow with rows x vocab.  With q = softmax(z / temperature)
+ * and weight[r] (fp32 [rows], NULL: 1),
+ *   loss[r]  = -weight[r] log q at targets[r];
+ *   stats[r] = (m, S) as mxq_token_logprobs writes them, S = sum exp((z - m) / temperature);
+ *   dz       = weight[r] / temperature (q - 1[v = target]),
+ *   dx = dz w,  dw = dz^T x,
+ * the gradients of the sum of the losses.  In the backward pass weight is the
+ * gradient of the unweighted loss.
+ *  - x [rows x hidden], w [vocab x hidden], dx, dw (as x, w) are bf16.  hidden is a
+ *    multiple of 32.  w and dw are 16-byte aligned, their leading dimensions
+ *    multiples of 8 and at most 2^22; x and dx stand at any element.  hidden is
+ *    at most 2^22, vocab less than 2^31 - 512, rows less than 2^31 - 255.
+ *  - Products of bf16 values are summed in fp32; dz is rounded to bf16 once,
+ *    dx and dw where they are stored.
+ *  - A row with a target < 0 or a weight of 0 does not count: loss 0, stats
+ *    (0, 1), dx 0, nothing in dw, whatever else it holds; and it costs nothing.  A
+ *    target >= vocab makes its row's loss and dx NaN, and dw with them.  Rows that
+ *    hold NaN or infinities follow the formulas (a row whose logits hold a NaN or
+ *    +inf has no distribution: S, loss and gradients NaN); the other rows' losses,
+ *    stats and dx are left alone.
+ *  - Sums run in a fixed order: repeated calls give the same bits.
+ *  - rows == 0: the forward pass does nothing, the backward pass clears dw.
+ *  - dx or dw may be NULL.  No output may overlap an input.
+ * workspace: 16-byte aligned, of the size that the functions below give (0 for
+ * sizes that are refused). */
+mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const void *w, int64_t ld_w,
+                                 int64_t rows, int64_t hidden, int64_t vocab, float temperature,
+                                 const int32_t *targets, const float *weight, float *loss,
+                                 float *stats, void *workspace, size_t ws_bytes, void *stream);
+size_t mxq_linear_ce_forward_workspace_size(int64_t rows, int64_t hidden, int64_t vocab);
+mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const void *w, int64_t ld_w,
+                                  int64_t rows, int64_t hidden, int64_t vocab, float temperature,
+                                  const int32_t *targets, const float *weight, const float *stats,
+                                  void *dx, int64_t ld_dx, void *dw, int64_t ld_dw,
+                                  void *workspace, size_t ws_bytes, void *stream);
+size_t mxq_linear_ce_backward_workspace_size(int64_t rows, int64_t hidden, int64_t vocab);
+
 /* Utilities (no passage defines them): a static description of a status
  * code, and the ABI version the library was built with (MXQ_ABI_VERSION). */
 const char *mxq_status_string(mxq_status s);
