@@ -1,0 +1,326 @@
+// The global norm of a list of gradients, and the gradients scaled down to a largest
+// norm.
+//
+//   sum_sq = sum over all elements of g^2,  norm = sqrt(sum_sq),
+//   c = min(1, max_norm / (norm + eps)),    out = c g.
+//
+// Both are bound by memory: one read for the norm, one read and one write for the
+// clipping.  The squares are summed in fp64, where they are exact and neither overflow
+// nor vanish; its two instructions an element hide behind the loads.
+//
+// The list goes to the kernels as an argument (no table in device memory that would have
+// to be copied there, or be kept), a batch of it a launch.  A workgroup takes one chunk of
+// one tensor, and finds it by counting the tensors that start at or before it.  The
+// workgroups' sums are added up by one workgroup in a fixed order.
+#include "mxq_host.hpp"
+#include "rows.hpp"
+#include "vocab.hpp"
+
+namespace mxq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 128;  // tensors of a launch: 3.6 KB of arguments
+constexpr int64_t kTypeBit = int64_t(1) << 62, kOutBit = int64_t(1) << 61;  // set: bf16
+constexpr int64_t kMostElements = int64_t(1) << 48;
+
+struct Batch {
+    const void *g[kBatch];
+    void *out[kBatch];
+    int64_t n[kBatch];       // and the types' bits
+    uint32_t first[kBatch];  // the tensor's first workgroup
+    int32_t count;
+    int32_t chunk;  // elements of a workgroup
+};
+
+// the tensor of workgroup w: the last that starts at or before it
+__device__ __forceinline__ int tensor_of(const Batch &b, uint32_t w)
+{
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; i += 64)
+        n += __popcll(__ballot(i + lane < b.count && b.first[i + lane] <= w));
+    return __builtin_amdgcn_readfirstlane(n) - 1;
+}
+
+// f(vector of E floats, index) for the workgroup's elements [0, n) at p, and f1(value, index)
+// for those behind the last whole vector
+constexpr int kAhead = 4;  // vectors of a thread in flight
+template <class T, bool ONCE, class F, class F1>
+__device__ __forceinline__ void for_elements(const T *p, int n, F f, F1 f1)
+{
+    constexpr int E = kElems<T>;
+    const int vectors = n / E;
+    int v = threadIdx.x;
+    for (; v + (kAhead - 1) * kThreads < vectors; v += kAhead * kThreads) {
+        gv4u raw[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            raw[i] = load_vec<ONCE>(p + (int64_t)(v + i * kThreads) * E);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            float x[E];
+            unpack(raw[i], x, (T *)nullptr);
+            f(x, (v + i * kThreads) * E);
+        }
+    }
+    for (; v < vectors; v += kThreads) {
+        float x[E];
+        unpack(load_vec<ONCE>(p + (int64_t)v * E), x, (T *)nullptr);
+        f(x, v * E);
+    }
+    const int rest = vectors * E + threadIdx.x;
+    if (rest < n)
+        f1(load_one(p + rest), rest);
+}
+
+template <class T> __device__ __forceinline__ double squares(const T *p, int n)
+{
+    double s[2] = {0.0, 0.0};
+    for_elements<T, false>(
+        p, n,
+        [&](const float(&x)[kElems<T>], int) {
+#pragma unroll
+            for (int j = 0; j < kElems<T>; ++j)
+                s[j & 1] = fma((double)x[j], (double)x[j], s[j & 1]);
+        },
+        [&](float x, int) { s[0] = fma((double)x, (double)x, s[0]); });
+    return s[0] + s[1];
+}
+
+__device__ __forceinline__ double wave_sum_double(double v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v += __shfl_xor(v, d);
+    return v;
+}
+template <int NT> __device__ __forceinline__ double block_sum_double(double v, double *lds)
+{
+    v = wave_sum_double(v);
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w)
+        s += lds[w];
+    return s;
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_squares(Batch b, double *part)
+{
+    __shared__ double lds[kThreads / 64];
+    const int t = tensor_of(b, blockIdx.x);
+    const int64_t from = (int64_t)(blockIdx.x - b.first[t]) * b.chunk;
+    const int64_t left = (b.n[t] & (kOutBit - 1)) - from;
+    const int n = (int)(left < b.chunk ? left : b.chunk);
+    const double s = b.n[t] & kTypeBit ? squares(static_cast<const bf16_t *>(b.g[t]) + from, n)
+                                       : squares(static_cast<const float *>(b.g[t]) + from, n);
+    const double all = block_sum_double<kThreads>(s, lds);
+    if (threadIdx.x == 0)
+        part[blockIdx.x] = all;
+}
+
+constexpr int kFinalThreads = 1024;
+__global__ __launch_bounds__(kFinalThreads) void k_grad_norm(const double *part, int64_t n,
+                                                             float *norm, double *sum_sq)
+{
+    __shared__ double lds[kFinalThreads / 64];
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    int64_t i = threadIdx.x;
+    for (; i + 3 * kFinalThreads < n; i += 4 * kFinalThreads)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            s[k] += part[i + k * kFinalThreads];
+    for (; i < n; i += kFinalThreads)
+        s[0] += part[i];
+    const double all = block_sum_double<kFinalThreads>((s[0] + s[1]) + (s[2] + s[3]), lds);
+    if (threadIdx.x == 0) {
+        if (sum_sq)
+            *sum_sq = all;
+        if (norm)
+            *norm = (float)sqrt(all);
+    }
+}
+
+// c as m 2^e, m an fp32 number in [1/2, 1]: c itself may be below fp32's normal numbers where c g
+// is not
+struct Scale {
+    float m;
+    int e;
+};
+template <class T, class O>
+__device__ __forceinline__ void scale_chunk(const T *p, O *out, int n, Scale c)
+{
+    for_elements<T, true>(
+        p, n,
+        [&](const float(&x)[kElems<T>], int at) {
+            float y[kElems<T>];
+#pragma unroll
+            for (int j = 0; j < kElems<T>; ++j)
+                y[j] = __builtin_ldexpf(x[j] * c.m, c.e);
+            store_vec(out + at, y);
+        },
+        [&](float x, int at) { out[at] = (O)__builtin_ldexpf(x * c.m, c.e); });
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_clip(Batch b, const double *sum_sq,
+                                                        float max_norm, float eps)
+{
+    const int t = tensor_of(b, blockIdx.x);
+    const int64_t from = (int64_t)(blockIdx.x - b.first[t]) * b.chunk;
+    const int64_t left = (b.n[t] & (kOutBit - 1)) - from;
+    const int n = (int)(left < b.chunk ? left : b.chunk);
+    const double q = (double)max_norm / (sqrt(*sum_sq) + (double)eps);
+    Scale c = {1.0f, 0};
+    if (!(q >= 1.0)) {  // NaN stays NaN
+        int e = 0;
+        c.m = (float)frexp(q, &e);
+        c.e = e;
+    } else if (b.out[t] == b.g[t]) {
+        return;
+    }
+    const bool wide = !(b.n[t] & kTypeBit), out_wide = !(b.n[t] & kOutBit);
+    const auto go = [&](auto *tt, auto *ot) {
+        using T = std::remove_pointer_t<decltype(tt)>;
+        using O = std::remove_pointer_t<decltype(ot)>;
+        scale_chunk(static_cast<const T *>(b.g[t]) + from, static_cast<O *>(b.out[t]) + from, n, c);
+    };
+    if (wide)
+        out_wide ? go((float *)nullptr, (float *)nullptr) : go((float *)nullptr, (bf16_t *)nullptr);
+    else
+        out_wide ? go((bf16_t *)nullptr, (float *)nullptr) : go((bf16_t *)nullptr, (bf16_t *)nullptr);
+}
+
+// ---- the host's side -------------------------------------------------------------
+
+// Elements of a workgroup, from all there are: enough workgroups for the chip first, then
+// fewer, longer ones.
+int chunk_of(int64_t elements)
+{
+    int chunk = 4096;
+    while (chunk < 32768 && elements / chunk > 4096)
+        chunk *= 2;
+    return chunk;
+}
+
+mxq_status check_grads(const mxq_grad *grads, int64_t count, bool out, int64_t &elements)
+{
+    elements = 0;
+    if (count < 0 || count > INT32_MAX)
+        return MXQ_ERR_SHAPE;
+    if (count > 0 && !grads)
+        return MXQ_ERR_NULL;
+    for (int64_t i = 0; i < count; ++i) {
+        const mxq_grad &g = grads[i];
+        if (!dtype_ok(g.dtype) || (out && !dtype_ok(g.out_dtype)))
+            return MXQ_ERR_UNSUPPORTED;
+        if (g.n < 0 || g.n > kMostElements || (elements += g.n) > kMostElements)
+            return MXQ_ERR_SHAPE;
+        if (g.n > 0 && (!g.g || (out && !g.out)))
+            return MXQ_ERR_NULL;
+        if (!aligned(g.g, g.dtype) || (out && !aligned(g.out, g.out_dtype)))
+            return MXQ_ERR_ALIGN;
+        if (out && g.out == g.g && g.out_dtype != g.dtype && g.n > 0)
+            return MXQ_ERR_UNSUPPORTED;
+    }
+    return MXQ_OK;
+}
+
+// launch(batch, workgroups) for the list, at most kBatch tensors at a time; the workgroups
+// of all launches.
+template <class F> int64_t for_batches(const mxq_grad *grads, int64_t count, int chunk, F launch)
+{
+    int64_t all = 0;
+    Batch b;
+    b.count = 0;
+    b.chunk = chunk;
+    uint32_t groups = 0;
+    const auto flush = [&] {
+        if (b.count > 0)
+            launch(b, groups);
+        all += groups;
+        b.count = 0;
+        groups = 0;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const mxq_grad &g = grads[i];
+        if (g.n == 0)
+            continue;
+        const int64_t need = (g.n + chunk - 1) / chunk;
+        if (b.count == kBatch || (b.count > 0 && groups + need > INT32_MAX))
+            flush();
+        b.g[b.count] = g.g;
+        b.out[b.count] = g.out;
+        b.n[b.count] = g.n | (g.dtype == MXQ_OUT_BF16 ? kTypeBit : 0) |
+                       (g.out_dtype == MXQ_OUT_BF16 ? kOutBit : 0);
+        b.first[b.count++] = groups;
+        groups += (uint32_t)need;
+    }
+    flush();
+    return all;
+}
+
+}  // namespace
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" size_t mxq_grad_norm_workspace_size(const mxq_grad *grads, int64_t count)
+{
+    int64_t elements;
+    if (check_grads(grads, count, false, elements))
+        return 0;
+    return 8 * (size_t)for_batches(grads, count, chunk_of(elements), [](const Batch &, uint32_t) {});
+}
+
+extern "C" mxq_status mxq_grad_norm(const mxq_grad *grads, int64_t count, float *norm,
+                                    double *sum_sq, void *workspace, size_t ws_bytes, void *stream)
+{
+    int64_t elements;
+    const mxq_status st = check_grads(grads, count, false, elements);
+    if (st)
+        return st;
+    if (!norm && !sum_sq)
+        return MXQ_ERR_NULL;
+    if (!aligned4(norm) || reinterpret_cast<uintptr_t>(sum_sq) % 8 ||
+        reinterpret_cast<uintptr_t>(workspace) % 8)
+        return MXQ_ERR_ALIGN;
+    const int chunk = chunk_of(elements);
+    const int64_t parts = for_batches(grads, count, chunk, [](const Batch &, uint32_t) {});
+    if (parts > 0 && (!workspace || ws_bytes < 8 * (size_t)parts))
+        return MXQ_ERR_WORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    double *part = static_cast<double *>(workspace);
+    for_batches(grads, count, chunk, [&](const Batch &b, uint32_t groups) {
+        hipLaunchKernelGGL(k_grad_squares, dim3(groups), dim3(kThreads), 0, s, b, part);
+        part += groups;
+    });
+    hipLaunchKernelGGL(k_grad_norm, dim3(1), dim3(kFinalThreads), 0, s,
+                       static_cast<const double *>(workspace), parts, norm, sum_sq);
+    return launched();
+}
+
+extern "C" mxq_status mxq_grad_clip(const mxq_grad *grads, int64_t count, const double *sum_sq,
+                                    float max_norm, float eps, void *stream)
+{
+    int64_t elements;
+    const mxq_status st = check_grads(grads, count, true, elements);
+    if (st)
+        return st;
+    if (!(max_norm >= 0.0f) || !(max_norm < INFINITY) || !(eps >= 0.0f) || !(eps < INFINITY))
+        return MXQ_ERR_UNSUPPORTED;
+    if (!sum_sq)
+        return MXQ_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(sum_sq) % 8)
+        return MXQ_ERR_ALIGN;
+    if (elements == 0)
+        return MXQ_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    for_batches(grads, count, chunk_of(elements), [&](const Batch &b, uint32_t groups) {
+        hipLaunchKernelGGL(k_grad_clip, dim3(groups), dim3(kThreads), 0, s, b, sum_sq, max_norm, eps);
+    });
+    return launched();
+}

@@ -29,7 +29,8 @@ SYMBOLS = ("mxq_quantize", "mxq_quantize_batch", "mxq_dequantize", "mxq_wgrad_ge
            "mxq_norm_forward", "mxq_norm_backward", "mxq_norm_backward_workspace_size", "mxq_token_logprobs",
            "mxq_token_logprobs_backward", "mxq_vocab_workspace_size", "mxq_distill_forward",
            "mxq_distill_backward", "mxq_distill", "mxq_linear_ce_forward", "mxq_linear_ce_forward_workspace_size",
-           "mxq_linear_ce_backward", "mxq_linear_ce_backward_workspace_size", "mxq_status_string", "mxq_abi_version")
+           "mxq_linear_ce_backward", "mxq_linear_ce_backward_workspace_size",
+           "mxq_grad_norm", "mxq_grad_norm_workspace_size", "mxq_grad_clip", "mxq_status_string", "mxq_abi_version")
 
 
 class QConfig(C.Structure):
@@ -42,6 +43,10 @@ class QConfig(C.Structure):
 class QTensor(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("fmt", C.c_int32),
                 ("grid", C.c_int32), ("layout", C.c_int32)]
+
+
+class Grad(C.Structure):
+    _fields_ = [("g", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32), ("out_dtype", C.c_int32)]
 
 
 class QuantizeJob(C.Structure):
@@ -115,6 +120,10 @@ def lib() -> C.CDLL:
         for name in ("mxq_linear_ce_forward_workspace_size", "mxq_linear_ce_backward_workspace_size"):
             getattr(L, name).argtypes = [i64, i64, i64]
             getattr(L, name).restype = sz
+        L.mxq_grad_norm.argtypes = [C.POINTER(Grad), i64, P, P, P, sz, P]
+        L.mxq_grad_norm_workspace_size.argtypes = [C.POINTER(Grad), i64]
+        L.mxq_grad_norm_workspace_size.restype = sz
+        L.mxq_grad_clip.argtypes = [C.POINTER(Grad), i64, P, f32, f32, P]
         L.mxq_status_string.argtypes = [i32]
         L.mxq_status_string.restype = C.c_char_p
         L.mxq_abi_version.restype = i32
@@ -122,7 +131,8 @@ def lib() -> C.CDLL:
                      "mxq_bias_stats", "mxq_bias_stats_noalloc", "mxq_round_to_grid", "mxq_rotate",
                      "mxq_norm_forward", "mxq_norm_backward", "mxq_token_logprobs",
                      "mxq_token_logprobs_backward", "mxq_distill_forward", "mxq_distill_backward",
-                     "mxq_distill", "mxq_linear_ce_forward", "mxq_linear_ce_backward"):
+                     "mxq_distill", "mxq_linear_ce_forward", "mxq_linear_ce_backward",
+                     "mxq_grad_norm", "mxq_grad_clip"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -755,3 +765,106 @@ def linear_ce_backward(x, w, targets, stats, weight=None, *, temperature=1, dx=T
         _vector("targets", targets, (rows,), x, torch.int32), _vector("weight", weight, (rows,), x),
         _vector("stats", stats, (rows, 2), x), dxp, lddx, dwp, lddw, _ptr(ws), size, handle))
     return dx, dw
+
+
+def _dense(t) -> bool:
+    """Whether t's elements lie side by side, each once, in whatever order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    at = 1
+    for stride, size in sorted((stride, size) for stride, size in zip(t.stride(), t.shape) if size != 1):
+        if stride != at:
+            return False
+        at *= size
+    return True
+
+
+def _grad_list(grads, out=None, write=True):
+    """The mxq_grad array of a list of tensors (written in place, or to the list `out`), and what it points into."""
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if not grads:
+        raise ValueError("no gradients: the device is theirs")
+    if len(out) != len(grads):
+        raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
+    first, seen = grads[0], set()
+    arr = (Grad * len(grads))()
+    for i, (g, o) in enumerate(zip(grads, out)):
+        for name, t in (("gradient", g), ("output", o)):
+            if t.device != first.device or not _dense(t):
+                raise ValueError(f"{name} {i}: a dense tensor on {first.device} expected, not strides {t.stride()} on {t.device}")
+        if o is not g and (o.shape != g.shape or o.stride() != g.stride()):
+            raise ValueError(f"output {i}: shape {tuple(o.shape)} strides {o.stride()}, not {tuple(g.shape)} {g.stride()}")
+        n = g.numel()
+        if write and n and o.data_ptr() in seen:
+            raise ValueError(f"output {i}: the same memory as another one")
+        seen.add(o.data_ptr())
+        arr[i] = Grad(g.data_ptr(), o.data_ptr(), n, _dtype(g), _dtype(o))
+    return arr, (grads, out)
+
+
+def prepare_grad_norm(grads):
+    """grad_norm(grads) marshalled once: a function that launches it on the current
+    stream (or `stream`) again and returns the same (norm, sum_sq) tensors.  It
+    holds the gradients and a workspace; calls of it that overlap race."""
+    arr, keep = _grad_list(grads, write=False)
+    first = keep[0][0]
+    torch, _ = _enter(first, None)
+    size = lib().mxq_grad_norm_workspace_size(arr, len(arr))
+    ws = first.new_empty(max(size, 8), dtype=torch.uint8)
+    norm, sum_sq = first.new_empty((), dtype=torch.float32), first.new_empty((), dtype=torch.float64)
+    ptrs = _ptr(norm), _ptr(sum_sq), _ptr(ws), size
+    fn = lib().mxq_grad_norm
+
+    def call(stream=None):
+        _check("mxq_grad_norm", fn(arr, len(arr), *ptrs, _enter(first, stream)[1]))
+        return norm, sum_sq
+    call._keep = (arr, keep, ws)
+    return call
+
+
+def prepare_clip_grad_norm(grads, max_norm, *, eps, out=None):
+    """clip_grad_norm(grads, max_norm) marshalled once: a function that launches it
+    on the current stream (or `stream`) again and returns the same norm tensor.  It
+    holds the gradients, the outputs and a workspace; calls of it that overlap race."""
+    arr, keep = _grad_list(grads, out)
+    first = keep[0][0]
+    measure = prepare_grad_norm(keep[0])
+    fn = lib().mxq_grad_clip
+
+    def call(stream=None):
+        norm, sum_sq = measure(stream)
+        _check("mxq_grad_clip", fn(arr, len(arr), _ptr(sum_sq), max_norm, eps, _enter(first, stream)[1]))
+        return norm
+    call._keep = (arr, keep, measure)
+    return call
+
+
+def grad_norm(grads, stream=None):
+    """mxq_grad_norm: (norm, sum_sq) over a list of tensors, fp32 and fp64 scalars."""
+    arr, keep = _grad_list(grads, write=False)
+    first = keep[0][0]
+    torch, handle = _enter(first, stream)
+    size = lib().mxq_grad_norm_workspace_size(arr, len(arr))
+    ws = _new(first, (max(size, 8),), torch.uint8, stream)
+    norm, sum_sq = _new(first, (), torch.float32, stream), _new(first, (), torch.float64, stream)
+    _check("mxq_grad_norm", lib().mxq_grad_norm(arr, len(arr), _ptr(norm), _ptr(sum_sq), _ptr(ws), size, handle))
+    return norm, sum_sq
+
+
+def grad_clip(grads, sum_sq, max_norm, *, eps, out=None, stream=None):
+    """mxq_grad_clip: the gradients scaled to max_norm by a sum of squares (fp64), in
+    place or into `out`, a list of tensors of the same shapes."""
+    arr, keep = _grad_list(grads, out)
+    first = keep[0][0]
+    torch, handle = _enter(first, stream)
+    _check("mxq_grad_clip", lib().mxq_grad_clip(
+        arr, len(arr), _vector("sum_sq", sum_sq, (), first, torch.float64), max_norm, eps, handle))
+
+
+def clip_grad_norm(grads, max_norm, *, eps, out=None, stream=None):
+    """grad_norm, then grad_clip by it; returns the norm."""
+    grads = list(grads)
+    norm, sum_sq = grad_norm(grads, stream)
+    grad_clip(grads, sum_sq, max_norm, eps=eps, out=out, stream=stream)
+    return norm

@@ -496,6 +496,39 @@ mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const void *w, in
                                   void *workspace, size_t ws_bytes, void *stream);
 size_t mxq_linear_ce_backward_workspace_size(int64_t rows, int64_t hidden, int64_t vocab);
 
+/* The global norm over a list of gradients, and their clipping to a largest
+ * norm, the last step in front of an optimizer:
+ *   sum_sq = sum over all elements of all tensors of g^2,  norm = sqrt(sum_sq);
+ *   c = min(1, max_norm / (norm + eps)),  out = c g.
+ * A tensor is n elements in a row from g, fp32 or bf16, at any element; out has
+ * the same number in its own type, and may be g itself (same type).  The list is
+ * a HOST array, read by the call.
+ *  - sum_sq (device, fp64) is summed in fp64 in a fixed order, norm (device,
+ *    fp32) is rounded from its root; either may be NULL.  Ranks that each hold a
+ *    part of the gradients add their sum_sq up between the two calls.
+ *  - c is formed in fp64 and rounded to fp32's 24 bits, c g rounded in fp32,
+ *    then to bf16 where out is.  Where c is 1, out is g; out == g is then left alone.
+ *  - A norm that is infinite gives c = 0, one that is NaN c = NaN, in IEEE
+ *    arithmetic (infinities become NaN, and everything does).
+ *  - Empty tensors and empty lists serve (norm 0).  An out may overlap no other
+ *    tensor's g or out.  max_norm and eps are finite and >= 0; where max_norm,
+ *    norm and eps are all 0, c is NaN.
+ *  - mxq_grad_norm only reads g, n and dtype.
+ * workspace: mxq_grad_norm_workspace_size(grads, count) bytes, 8-byte aligned (0
+ * for empty lists and those that are refused). */
+typedef struct {
+    const void *g;
+    void *out;
+    int64_t n;
+    int32_t dtype;      /* MXQ_OUT_* of g */
+    int32_t out_dtype;  /* MXQ_OUT_* of out */
+} mxq_grad;
+mxq_status mxq_grad_norm(const mxq_grad *grads, int64_t count, float *norm, double *sum_sq,
+                         void *workspace, size_t ws_bytes, void *stream);
+size_t mxq_grad_norm_workspace_size(const mxq_grad *grads, int64_t count);
+mxq_status mxq_grad_clip(const mxq_grad *grads, int64_t count, const double *sum_sq,
+                         float max_norm, float eps, void *stream);
+
 /* Utilities (no passage defines them): a static description of a status
  * code, and the ABI version the library was built with (MXQ_ABI_VERSION). */
 const char *mxq_status_string(mxq_status s);
