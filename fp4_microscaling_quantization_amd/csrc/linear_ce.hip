@@ -119,11 +119,10 @@ template <class Tile>
 __device__ __forceinline__ void logits(Tile &t, uint8_t *lds, const CeWeight &w, const u16 *x,
                                        int p0, int count, int q0)
 {
-    t.start(w.ld, w.vocab - p0, w.hidden, count - q0);
+    t.start(lds, w.ld, w.vocab - p0, w.hidden, count - q0);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)p0 * w.ld);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(x + (int64_t)q0 * w.hidden);
-    t.run(lds, w.hidden / kStepK, [&](int s) { return p + s * (kStepK * 2); },
-          [&](int s) { return q + s * (kStepK * 2); });
+    t.run(w.hidden / kStepK, p, kStepK * 2, q, kStepK * 2);
 }
 
 // Maximum and sum of every packed row over the tile's vocabulary, and the logit at its
@@ -283,11 +282,10 @@ __global__ __launch_bounds__(Dx::kThreads, 1) void k_ce_dx(CeWeight w, CePacked 
     Dx t;
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)(piece0 + v0) * w.ld + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + (int64_t)q0 * width + v0);
-    t.start(w.ld, w.hidden - p0, width, Dx::kQ);
+    t.start(lds, w.ld, w.hidden - p0, width, Dx::kQ);
     // dz is zero behind the vocabulary's last
-    t.cut_p(have, w.ld, w.hidden - p0);
-    t.run(lds, n, [&](int s) { return p + s * (kStepK * w.ld * 2); },
-          [&](int s) { return q + s * (kStepK * 2); });
+    t.cut(max(0, have), w.ld, w.hidden - p0);
+    t.run(n, p, kStepK * 2 * (uint32_t)w.ld, q, kStepK * 2);
     float *to = sums + blockIdx.y * slab;
 #pragma unroll
     for (int j = 0; j < Dx::NQ; ++j)
@@ -333,11 +331,10 @@ __global__ __launch_bounds__(Dw::kThreads, 1) void k_ce_dw(CeWeight w, CePacked 
     product_tile(blockIdx.x, np, nq, tp, tq);
     const int p0 = tp * Dw::kP, q0 = tq * Dw::kQ;
     Dw t;
-    t.start(w.hidden, w.hidden - p0, width, width - q0);
+    t.start(lds, w.hidden, w.hidden - p0, width, width - q0);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(x.x + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + q0);
-    t.run(lds, (*x.count + kStepK - 1) / kStepK, [&](int s) { return p + (int64_t)s * (kStepK * 2) * w.hidden; },
-          [&](int s) { return q + (int64_t)s * (kStepK * 2) * width; });
+    t.run((*x.count + kStepK - 1) / kStepK, p, kStepK * 2 * w.hidden, q, kStepK * 2 * width);
 #pragma unroll
     for (int j = 0; j < Dw::NQ; ++j)
 #pragma unroll
