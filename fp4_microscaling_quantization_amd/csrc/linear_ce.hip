@@ -33,7 +33,8 @@ struct CePacked {
     int *place;        // [rows]: a row's place among them, -1: none
     int *row;          // [count]
     float *at_target;  // [count]: the logit at the target
-    u16 *x;            // [count, up to the next multiple of 32][hidden]
+    u16 *x;            // [count, up to a whole step][ld], zero behind both
+    int ld;            // hidden, up to a whole step
 };
 
 // the statistics of two stretches of a row, as one
@@ -55,9 +56,9 @@ __device__ __forceinline__ bool row_counts(const CeRows &a, int64_t r)
 constexpr int kPackThreads = 256;
 
 // The rows that count, in order: where each went (or -1), which it was, and how many,
-// and (with x) their values.  A workgroup finds its place by counting all rows in front
-// of its own.  Up to the next multiple of 32 rows are zero, which the product over the
-// rows reads.
+// and their values.  A workgroup finds its place by counting all rows in front of its
+// own.  Behind the last row and the last value are zeros, up to whole steps of the
+// products over either.
 __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per, const bf16_t *x,
                                                           int64_t ld, int hidden, CePacked to)
 {
@@ -87,26 +88,22 @@ __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per,
             if (in)
                 to.row[at] = (int)mine;
         }
-        if (x) {
-            int n = place;
-            for (uint64_t left = all; left; left &= left - 1, ++n) {
-                const int64_t r = base + __builtin_ctzll(left);
-                for (int c = threadIdx.x * 8; c < hidden; c += kPackThreads * 8)
-                    *reinterpret_cast<gv4u *>(to.x + (int64_t)n * hidden + c) =
-                        load_vec(x + r * ld + c);
-            }
+        int n = place;
+        for (uint64_t left = all; left; left &= left - 1, ++n) {
+            const int64_t r = base + __builtin_ctzll(left);
+            for (int c = threadIdx.x * 8; c < to.ld; c += kPackThreads * 8)
+                *reinterpret_cast<gv4u *>(to.x + (int64_t)n * to.ld + c) =
+                    c < hidden ? load_vec(x + r * ld + c) : (gv4u){0u, 0u, 0u, 0u};
         }
         place += __popcll(all);
     }
     if (blockIdx.x == gridDim.x - 1) {
         if (threadIdx.x == 0)
             *to.count = place;
-        if (x) {
-            const int stop = (place + kStepK - 1) / kStepK * kStepK;
-            for (int64_t c = (int64_t)place * hidden + threadIdx.x * 8; c < (int64_t)stop * hidden;
-                 c += kPackThreads * 8)
-                *reinterpret_cast<gv4u *>(to.x + c) = (gv4u){0u, 0u, 0u, 0u};
-        }
+        const int stop = (place + kStepK - 1) / kStepK * kStepK;
+        for (int64_t c = (int64_t)place * to.ld + threadIdx.x * 8; c < (int64_t)stop * to.ld;
+             c += kPackThreads * 8)
+            *reinterpret_cast<gv4u *>(to.x + c) = (gv4u){0u, 0u, 0u, 0u};
     }
 }
 
@@ -116,13 +113,13 @@ using Logit = Product<2, 4, 8, 4, true, true>;
 
 // the tile's product: w rows from p0, packed x rows from q0
 template <class Tile>
-__device__ __forceinline__ void logits(Tile &t, uint8_t *lds, const CeWeight &w, const u16 *x,
-                                       int p0, int count, int q0)
+__device__ __forceinline__ void logits(Tile &t, uint8_t *lds, const CeWeight &w,
+                                       const CePacked &x, int p0, int count, int q0)
 {
-    t.start(lds, w.ld, w.vocab - p0, w.hidden, count - q0);
+    t.start(lds, w.ld, w.vocab - p0, x.ld, count - q0, w.hidden);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)p0 * w.ld);
-    const uint8_t *q = reinterpret_cast<const uint8_t *>(x + (int64_t)q0 * w.hidden);
-    t.run(w.hidden / kStepK, p, kStepK * 2, q, kStepK * 2);
+    const uint8_t *q = reinterpret_cast<const uint8_t *>(x.x + (int64_t)q0 * x.ld);
+    t.run(x.ld / kStepK, p, kStepK * 2, q, kStepK * 2);
 }
 
 // Maximum and sum of every packed row over the tile's vocabulary, and the logit at its
@@ -140,7 +137,7 @@ __global__ __launch_bounds__(Logit::kThreads, 1) void k_ce_stats(CeWeight w, CeR
     product_tile(blockIdx.x, np, nq, tp, tq);
     const int p0 = tp * Logit::kP, q0 = tq * Logit::kQ;
     Logit t;
-    logits(t, lds, w, x.x, p0, count, q0);
+    logits(t, lds, w, x, p0, count, q0);
 
     __syncthreads();
     float2 *joint = reinterpret_cast<float2 *>(lds);  // [WP][kQ]
@@ -231,7 +228,7 @@ __global__ __launch_bounds__(Logit::kThreads, 1) void k_ce_dlogits(CeWeight w, C
     product_tile(blockIdx.x, np, nq, tp, tq);
     const int p0 = piece0 + tp * Logit::kP, q0 = tq * Logit::kQ;
     Logit t;
-    logits(t, lds, w, x.x, p0, count, q0);
+    logits(t, lds, w, x, p0, count, q0);
 #pragma unroll
     for (int j = 0; j < Logit::NQ; ++j) {
         const int q = q0 + t.q_of(j);
@@ -282,9 +279,7 @@ __global__ __launch_bounds__(Dx::kThreads, 1) void k_ce_dx(CeWeight w, CePacked 
     Dx t;
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)(piece0 + v0) * w.ld + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + (int64_t)q0 * width + v0);
-    t.start(lds, w.ld, w.hidden - p0, width, Dx::kQ);
-    // dz is zero behind the vocabulary's last
-    t.cut(max(0, have), w.ld, w.hidden - p0);
+    t.start(lds, w.ld, w.hidden - p0, width, Dx::kQ, max(0, have));
     t.run(n, p, kStepK * 2 * (uint32_t)w.ld, q, kStepK * 2);
     float *to = sums + blockIdx.y * slab;
 #pragma unroll
@@ -331,10 +326,10 @@ __global__ __launch_bounds__(Dw::kThreads, 1) void k_ce_dw(CeWeight w, CePacked 
     product_tile(blockIdx.x, np, nq, tp, tq);
     const int p0 = tp * Dw::kP, q0 = tq * Dw::kQ;
     Dw t;
-    t.start(lds, w.hidden, w.hidden - p0, width, width - q0);
+    t.start(lds, x.ld, x.ld - p0, width, width - q0, kStepK);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(x.x + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + q0);
-    t.run((*x.count + kStepK - 1) / kStepK, p, kStepK * 2 * w.hidden, q, kStepK * 2 * width);
+    t.run((*x.count + kStepK - 1) / kStepK, p, kStepK * 2 * x.ld, q, kStepK * 2 * width);
 #pragma unroll
     for (int j = 0; j < Dw::NQ; ++j)
 #pragma unroll
@@ -372,7 +367,8 @@ CePacked take_packed(Carve &c, int64_t rows, int64_t hidden)
     x.place = c.take<int>(rows);
     x.row = c.take<int>(rows);
     x.at_target = c.take<float>(rows);
-    x.x = c.take<u16>(up(rows, kStepK) * hidden);
+    x.ld = (int)up(hidden, kStepK);
+    x.x = c.take<u16>(up(rows, kStepK) * x.ld);
     return x;
 }
 
