@@ -119,7 +119,8 @@ __device__ __forceinline__ void logits(Tile &t, uint8_t *lds, const CeWeight &w,
     t.start(lds, w.ld, w.vocab - p0, x.ld, count - q0, w.hidden);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)p0 * w.ld);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(x.x + (int64_t)q0 * x.ld);
-    t.run(x.ld / kStepK, p, kStepK * 2, q, kStepK * 2);
+    const int steps = (w.hidden + kStepK - 1) / kStepK;
+    t.run(steps, p, kStepK * 2, q, kStepK * 2, (int)(blockIdx.x & 7) * steps / 8);
 }
 
 // Maximum and sum of every packed row over the tile's vocabulary, and the logit at its
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(256) void k_ce_loss(CeRows a, CePacked x, int vocab
 __global__ __launch_bounds__(Logit::kThreads, 1) void k_ce_dlogits(CeWeight w, CeRows a,
                                                                    CePacked x, Heat heat,
                                                                    const float2 *stats, int piece0,
-                                                                   int width, u16 *dz)
+                                                                   int width, u16 *dz, int ld)
 {
     __shared__ __align__(16) uint8_t lds[Logit::kLds];
     const int count = *x.count;
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(Logit::kThreads, 1) void k_ce_dlogits(CeWeight w, C
             scale = NAN;
         const float base = base_of(st.x);
         const float inv = st.y == 0.0f ? 0.0f : scale / st.y;
-        u16 *to = dz + (int64_t)q * width + tp * Logit::kP;
+        u16 *to = dz + (int64_t)q * ld + tp * Logit::kP;
 #pragma unroll
         for (int i = 0; i < Logit::NP; ++i) {
             float d[4];
@@ -262,7 +263,7 @@ using Dx = Product<2, 4, 8, 4, false, true>;
 // A part of dx = dz w: the products of a stretch of the piece's vocabulary, added to
 // (or, for the first piece, written as) slab blockIdx.y of fp32 sums.
 __global__ __launch_bounds__(Dx::kThreads, 1) void k_ce_dx(CeWeight w, CePacked x, int piece0,
-                                                           int width, int steps, const u16 *dz,
+                                                           int width, int steps, const u16 *dz, int ld,
                                                            float *sums, int64_t slab, int add)
 {
     __shared__ __align__(16) uint8_t lds[Dx::kLds];
@@ -278,8 +279,8 @@ __global__ __launch_bounds__(Dx::kThreads, 1) void k_ce_dx(CeWeight w, CePacked 
     const int n = max(0, min(steps, (have + kStepK - 1) / kStepK));
     Dx t;
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)(piece0 + v0) * w.ld + p0);
-    const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + (int64_t)q0 * width + v0);
-    t.start(lds, w.ld, w.hidden - p0, width, Dx::kQ, max(0, have));
+    const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + (int64_t)q0 * ld + v0);
+    t.start(lds, w.ld, w.hidden - p0, ld, Dx::kQ, max(0, have));
     t.run(n, p, kStepK * 2 * (uint32_t)w.ld, q, kStepK * 2);
     float *to = sums + blockIdx.y * slab;
 #pragma unroll
@@ -315,8 +316,8 @@ using Dw = Product<2, 4, 8, 4, false, false>;
 
 // dw = dz^T x of a piece of the vocabulary
 __global__ __launch_bounds__(Dw::kThreads, 1) void k_ce_dw(CeWeight w, CePacked x, int piece0,
-                                                           int width, const u16 *dz, u16 *dw,
-                                                           int64_t ld)
+                                                           int width, const u16 *dz, int ld,
+                                                           u16 *dw, int64_t ld_dw)
 {
     __shared__ __align__(16) uint8_t lds[Dw::kLds];
     const int np = (w.hidden + Dw::kP - 1) / Dw::kP;
@@ -326,17 +327,17 @@ __global__ __launch_bounds__(Dw::kThreads, 1) void k_ce_dw(CeWeight w, CePacked 
     product_tile(blockIdx.x, np, nq, tp, tq);
     const int p0 = tp * Dw::kP, q0 = tq * Dw::kQ;
     Dw t;
-    t.start(lds, x.ld, x.ld - p0, width, width - q0, kStepK);
+    t.start(lds, x.ld, x.ld - p0, ld, width - q0, kStepK);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(x.x + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + q0);
-    t.run((*x.count + kStepK - 1) / kStepK, p, kStepK * 2 * x.ld, q, kStepK * 2 * width);
+    t.run((*x.count + kStepK - 1) / kStepK, p, kStepK * 2 * x.ld, q, kStepK * 2 * ld);
 #pragma unroll
     for (int j = 0; j < Dw::NQ; ++j)
 #pragma unroll
         for (int i = 0; i < Dw::NP; ++i) {
             const int q1 = q0 + t.q_of(j), p1 = p0 + t.p_of(i);
             if (q1 < have && p1 < w.hidden)
-                *reinterpret_cast<gv2u *>(dw + (int64_t)(piece0 + q1) * ld + p1) =
+                *reinterpret_cast<gv2u *>(dw + (int64_t)(piece0 + q1) * ld_dw + p1) =
                     (gv2u){pack_bf16(t.acc[i][j][0], t.acc[i][j][1]), pack_bf16(t.acc[i][j][2], t.acc[i][j][3])};
         }
 }
@@ -360,6 +361,10 @@ struct Carve {
     }
 };
 
+// A leading dimension of workspace rows of n values: not a multiple of 2 KiB, whose lines of
+// one k would share the L2's channels.  x.ld counts them in the zeros behind a row's values.
+int64_t pitch(int64_t n) { return n % 1024 ? n : n + kStepK; }
+
 CePacked take_packed(Carve &c, int64_t rows, int64_t hidden)
 {
     CePacked x;
@@ -367,7 +372,7 @@ CePacked take_packed(Carve &c, int64_t rows, int64_t hidden)
     x.place = c.take<int>(rows);
     x.row = c.take<int>(rows);
     x.at_target = c.take<float>(rows);
-    x.ld = (int)up(hidden, kStepK);
+    x.ld = (int)pitch(up(hidden, kStepK));
     x.x = c.take<u16>(up(rows, kStepK) * x.ld);
     return x;
 }
@@ -394,7 +399,7 @@ struct BackwardPlan {
     CePacked x;
     u16 *dz;
     float *sums;
-    int64_t width, pieces, slab, slabs, steps;
+    int64_t width, ld, pieces, slab, slabs, steps;
     size_t bytes;
 };
 BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
@@ -409,7 +414,8 @@ BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws
     b.pieces = (vocab + width - 1) / width;
     b.width = up((vocab + b.pieces - 1) / b.pieces, Logit::kP);
     b.pieces = (vocab + b.width - 1) / b.width;
-    b.dz = c.take<u16>(padded * b.width);
+    b.ld = pitch(b.width);
+    b.dz = c.take<u16>(padded * b.ld);
     // the vocabulary in stretches until the products for dx fill the chip
     const int64_t tiles = (hidden + Dx::kP - 1) / Dx::kP * (padded / Dx::kQ);
     const int64_t room = b.width / 512 > 0 ? b.width / 512 : 1;
@@ -546,15 +552,15 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
             const int64_t np = (have + Logit::kP - 1) / Logit::kP;
             hipLaunchKernelGGL(k_ce_dlogits, dim3((unsigned)(np * nq)), dim3(Logit::kThreads), 0, s,
                                cw, a, b.x, heat, reinterpret_cast<const float2 *>(stats), piece0,
-                               (int)b.width, b.dz);
+                               (int)b.width, b.dz, (int)b.ld);
             if (dx)
                 hipLaunchKernelGGL(k_ce_dx, dim3((unsigned)x_tiles, (unsigned)b.slabs),
                                    dim3(Dx::kThreads), 0, s, cw, b.x, piece0, (int)b.width,
-                                   (int)b.steps, b.dz, b.sums, b.slab, i > 0);
+                                   (int)b.steps, b.dz, (int)b.ld, b.sums, b.slab, i > 0);
         }
         if (dw)
             hipLaunchKernelGGL(k_ce_dw, dim3((unsigned)w_tiles), dim3(Dw::kThreads), 0, s, cw, b.x,
-                               piece0, (int)b.width, b.dz, static_cast<u16 *>(dw), ld_dw);
+                               piece0, (int)b.width, b.dz, (int)b.ld, static_cast<u16 *>(dw), ld_dw);
     }
     if (dx && rows > 0)
         hipLaunchKernelGGL(k_ce_dx_rows, dim3((unsigned)rows), dim3(256), 0, s, rows, (int)hidden,

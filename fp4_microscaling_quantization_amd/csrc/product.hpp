@@ -222,21 +222,26 @@ template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct
     // slot has been read when its first half is done: there, once a step, is the barrier,
     // and the step after the next is fetched behind it into the same slot.  It lands
     // during the second half and the next step's first one.
+    // The steps are taken in a circle from step `first`.
     __device__ __forceinline__ void run(int steps, const uint8_t *p, uint32_t dp, const uint8_t *q,
-                                        uint32_t dq)
+                                        uint32_t dq, int first = 0)
     {
         if (steps <= 0)
             return;
         steps = __builtin_amdgcn_readfirstlane(steps);
         p = uniform(p);
         q = uniform(q);
+        int at = __builtin_amdgcn_readfirstlane(first);  // the step that is fetched next
+        const auto next = [&] { at = at + 1 < steps ? at + 1 : 0; };
 #pragma unroll
         for (int n = 0; n < kPer; ++n)
-            copy(n, 0, 0, p, q);
+            copy(n, at, 0, p + (uint64_t)(uint32_t)at * dp, q + (uint64_t)(uint32_t)at * dq);
+        next();
         if (steps > 1) {
 #pragma unroll
             for (int n = 0; n < kPer; ++n)
-                copy(n, 1, 1, p + dp, q + dq);
+                copy(n, at, 1, p + (uint64_t)(uint32_t)at * dp, q + (uint64_t)(uint32_t)at * dq);
+            next();
             __builtin_amdgcn_s_waitcnt(0x0070 | kPer);
         } else {
             __builtin_amdgcn_s_waitcnt(0x0070);
@@ -262,16 +267,18 @@ template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct
                 __builtin_amdgcn_sched_barrier(0);
                 read_p.move(slot ? -SideP::kBytes : SideP::kBytes);
                 read_q.move(slot ? -SideQ::kBytes : SideQ::kBytes);
-                const uint8_t *ps = p + (uint64_t)(uint32_t)(s + 2) * dp;
-                const uint8_t *qs = q + (uint64_t)(uint32_t)(s + 2) * dq;
+                const uint8_t *ps = p + (uint64_t)(uint32_t)at * dp;
+                const uint8_t *qs = q + (uint64_t)(uint32_t)at * dq;
                 constexpr int COPIES = COPY ? kPer : 0;
                 products<FRAGMENTS + COPIES>(fp[1], fq[1], [&](int n) {
                     // a copy and a fragment in turn, copies first: they take longest
                     if (n < 2 * COPIES ? n % 2 == 0 : false)
-                        copy(n / 2, s + 2, slot, ps, qs);
+                        copy(n / 2, at, slot, ps, qs);
                     else
                         fragment(n < 2 * COPIES ? n / 2 : n - COPIES, 0, fp[0], fq[0]);
                 });
+                if constexpr (COPY)
+                    next();
             }
         };
         constexpr std::true_type yes{};
@@ -291,21 +298,20 @@ template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct
     __device__ __forceinline__ int q_of(int j) const { return 16 * (wq + WQ * j) + (lane & 15); }
 };
 
-// Tile (tp, tq) of workgroup w of np x nq.  Workgroups go round-robin over the 8 XCDs;
-// each XCD gets a contiguous run of tiles, four tiles of q deep, so that the tiles that
-// share an XCD's L2 share panels of both operands.
+// Tile (tp, tq) of workgroup w of np x nq.  Workgroups go round-robin over the 8 XCDs, so
+// in a band of eight tiles of p each XCD gets nq tiles, neighbours in q: the 32 CUs of an
+// XCD share eight panels of P and nq / 8 of Q in its L2, and all XCDs read the same eight
+// panels of P at a time.  (A contiguous run of all tiles for each XCD reads P once for each
+// from HBM unless nq is a multiple of 32: 8192 x 4096 x 128256 with 29 tiles of q 6.2 ms
+// against 5.7.)
 __device__ __forceinline__ void product_tile(int w, int np, int nq, int &tp, int &tq)
 {
-    const int total = np * nq;
-    const int whole = total / 8 * 8;
-    if (w < whole)
-        w = (w % 8) * (total / 8) + w / 8;
-    constexpr int DEEP = 4;
-    const int first = w / (DEEP * np) * DEEP;
-    const int deep = min(nq - first, DEEP);
-    const int loc = w - first * np;
-    tq = first + loc % deep;
-    tp = loc / deep;
+    const int band = w / (8 * nq) * 8;
+    const int wide = min(8, np - band);
+    const int loc = w - band * nq, all = wide * nq;
+    const int place = loc < all / 8 * 8 ? (loc % 8) * (all / 8) + loc / 8 : loc;
+    tq = place / wide;
+    tp = band + place % wide;
 }
 
 }  // namespace mxq
