@@ -55,35 +55,52 @@ __device__ __forceinline__ bool row_counts(const CeRows &a, int64_t r)
 
 constexpr int kPackThreads = 256;
 
-// The rows that count, in order: where each went (or -1), which it was, and how many,
-// and their values.  A workgroup finds its place by counting all rows in front of its
-// own.  Behind the last row and the last value are zeros, up to whole steps of the
-// products over either.
-__global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per, const bf16_t *x,
-                                                          int64_t ld, int hidden, CePacked to)
+// The sum over the workgroup of a count
+__device__ __forceinline__ int block_count(int n)
 {
     __shared__ int partial[kPackThreads / 64];
-    const int64_t first = (int64_t)blockIdx.x * per;
-    const int64_t end = first + per < a.rows ? first + per : a.rows;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    int before = 0;
-    for (int64_t r = threadIdx.x; r < first; r += kPackThreads)
-        before += row_counts(a, r);
     for (int d = 1; d < 64; d *= 2)
-        before += __shfl_xor(before, d);
-    if (lane == 0)
-        partial[wave] = before;
+        n += __shfl_xor(n, d);
+    if ((threadIdx.x & 63) == 0)
+        partial[threadIdx.x >> 6] = n;
     __syncthreads();
-    int place = 0;
+    n = 0;
     for (int w = 0; w < kPackThreads / 64; ++w)
-        place += partial[w];
+        n += partial[w];
+    return n;
+}
+
+// The rows that count, in order: where each went (or -1), which it was, how many, and
+// their values, with zeros behind the last value up to a whole step.  A workgroup takes
+// `per` rows, and finds their place by counting all rows in front of them.  The ones
+// behind `groups` write zeros behind the last row up to a whole step, which the product
+// over the rows reads, a row each.
+__global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per, int groups,
+                                                          const bf16_t *x, int64_t ld, int hidden,
+                                                          CePacked to)
+{
+    const int lane = threadIdx.x & 63;
+    const bool behind = (int)blockIdx.x >= groups;
+    const int64_t first = behind ? a.rows : (int64_t)blockIdx.x * per;
+    const int64_t end = first + per < a.rows ? first + per : a.rows;
+    int place = 0;
+    for (int64_t r = threadIdx.x; r < first; r += kPackThreads)
+        place += row_counts(a, r);
+    place = block_count(place);
+    if (behind) {
+        const int row = place + (int)blockIdx.x - groups;
+        if (row < (place + kStepK - 1) / kStepK * kStepK)
+            for (int c = threadIdx.x * 8; c < to.ld; c += kPackThreads * 8)
+                *reinterpret_cast<gv4u *>(to.x + (int64_t)row * to.ld + c) = (gv4u){0u, 0u, 0u, 0u};
+        return;
+    }
     for (int64_t base = first; base < end; base += 64) {
         // every wave works out the same
         const int64_t mine = base + lane;
         const bool in = mine < end && row_counts(a, mine);
         const uint64_t all = __ballot(in);
         const int at = place + __popcll(all & ((1ull << lane) - 1));
-        if (wave == 0 && mine < end) {
+        if (threadIdx.x < 64 && mine < end) {
             to.place[mine] = in ? at : -1;
             if (in)
                 to.row[at] = (int)mine;
@@ -97,26 +114,25 @@ __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per,
         }
         place += __popcll(all);
     }
-    if (blockIdx.x == gridDim.x - 1) {
-        if (threadIdx.x == 0)
-            *to.count = place;
-        const int stop = (place + kStepK - 1) / kStepK * kStepK;
-        for (int64_t c = (int64_t)place * to.ld + threadIdx.x * 8; c < (int64_t)stop * to.ld;
-             c += kPackThreads * 8)
-            *reinterpret_cast<gv4u *>(to.x + c) = (gv4u){0u, 0u, 0u, 0u};
-    }
+    if ((int)blockIdx.x == groups - 1 && threadIdx.x == 0)
+        *to.count = place;
 }
 
 // ---- logits ----------------------------------------------------------------------
 
-using Logit = Product<2, 4, 8, 4, true, true>;
+// Tiles for many rows, and for few, where the weight is what there is to read: one wave
+// wide in the rows, several workgroups a CU.
+template <bool P_ALONG, bool Q_ALONG> using Many = Product<2, 4, 8, 4, P_ALONG, Q_ALONG>;  // 256 x 256
+template <bool P_ALONG, bool Q_ALONG> using Some = Product<4, 1, 2, 8, P_ALONG, Q_ALONG>;  // 128 x 128
+template <bool P_ALONG, bool Q_ALONG> using Few = Product<4, 1, 2, 2, P_ALONG, Q_ALONG>;   // 128 x 32
 
 // the tile's product: w rows from p0, packed x rows from q0
 template <class Tile>
 __device__ __forceinline__ void logits(Tile &t, uint8_t *lds, const CeWeight &w,
                                        const CePacked &x, int p0, int count, int q0)
 {
-    t.start(lds, w.ld, w.vocab - p0, x.ld, count - q0, w.hidden);
+    const int rows = (count + kStepK - 1) / kStepK * kStepK;
+    t.start(lds, w.ld, w.vocab - p0, x.ld, rows - q0, w.hidden);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)p0 * w.ld);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(x.x + (int64_t)q0 * x.ld);
     const int steps = (w.hidden + kStepK - 1) / kStepK;
@@ -125,77 +141,110 @@ __device__ __forceinline__ void logits(Tile &t, uint8_t *lds, const CeWeight &w,
 
 // Maximum and sum of every packed row over the tile's vocabulary, and the logit at its
 // target.
-__global__ __launch_bounds__(Logit::kThreads, 1) void k_ce_stats(CeWeight w, CeRows a,
-                                                                 CePacked x, Heat heat,
-                                                                 float2 *part, int64_t stride)
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_stats(CeWeight w, CeRows a, CePacked x,
+                                                                Heat heat, float2 *part,
+                                                                int64_t stride)
 {
-    __shared__ __align__(16) uint8_t lds[Logit::kLds];
+    __shared__ __align__(16) uint8_t lds[Tile::kLds];
     const int count = *x.count;
-    const int np = (w.vocab + Logit::kP - 1) / Logit::kP, nq = (count + Logit::kQ - 1) / Logit::kQ;
+    const int np = (w.vocab + Tile::kP - 1) / Tile::kP, nq = (count + Tile::kQ - 1) / Tile::kQ;
     if ((int)blockIdx.x >= np * nq)
         return;
     int tp, tq;
     product_tile(blockIdx.x, np, nq, tp, tq);
-    const int p0 = tp * Logit::kP, q0 = tq * Logit::kQ;
-    Logit t;
+    const int p0 = tp * Tile::kP, q0 = tq * Tile::kQ;
+    Tile t;
     logits(t, lds, w, x, p0, count, q0);
 
-    __syncthreads();
     float2 *joint = reinterpret_cast<float2 *>(lds);  // [WP][kQ]
+    const bool whole = p0 + Tile::kP <= w.vocab;
 #pragma unroll
-    for (int j = 0; j < Logit::NQ; ++j) {
+    for (int j = 0; j < Tile::NQ; ++j) {
         const int q = t.q_of(j);
-        const int target = q0 + q < count ? a.targets[x.row[q0 + q]] : -1;
+        const int target = q0 + q < count ? a.targets[x.row[q0 + q]] - p0 : -1;
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < Tile::NP; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (p0 + t.p_of(i) + r >= w.vocab)
+                        t.acc[i][j][r] = -INFINITY;
+        }
+        // few tiles hold a target of theirs
+        if (__any((unsigned)target < (unsigned)Tile::kP)) {
+#pragma unroll
+            for (int i = 0; i < Tile::NP; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (t.p_of(i) + r == target && p0 + target < w.vocab)
+                        x.at_target[q0 + q] = t.acc[i][j][r];
+        }
         float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < Logit::NP; ++i)
+        for (int i = 0; i < Tile::NP; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int p = p0 + t.p_of(i) + r;
-                if (p >= w.vocab)
-                    t.acc[i][j][r] = -INFINITY;
-                if (p == target)
-                    x.at_target[q0 + q] = t.acc[i][j][r];
+            for (int r = 0; r < 4; ++r)
                 m = fmaxf(m, t.acc[i][j][r]);
-            }
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
         const float base = base_of(m);
-        float s = 0.0f;
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < Logit::NP; ++i)
+        for (int i = 0; i < Tile::NP; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                s += __builtin_amdgcn_exp2f((t.acc[i][j][r] - base) * heat.log2);
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
+                s[r & 1] += __builtin_amdgcn_exp2f((t.acc[i][j][r] - base) * heat.log2);
+        s[0] += s[1];
+        s[0] += __shfl_xor(s[0], 16);
+        s[0] += __shfl_xor(s[0], 32);
         if (t.lane < 16)
-            joint[t.wp * Logit::kQ + q] = make_float2(m, s);
+            joint[t.wp * Tile::kQ + q] = make_float2(m, s[0]);
     }
     __syncthreads();
-    for (int q = threadIdx.x; q < Logit::kQ && q0 + q < count; q += Logit::kThreads) {
+    for (int q = threadIdx.x; q < Tile::kQ && q0 + q < count; q += Tile::kThreads) {
         RowStats st = {joint[q].x, joint[q].y, 0.0f};
-        for (int k = 1; k < Logit::WP; ++k)
-            join_stats(st, joint[k * Logit::kQ + q], heat.log2);
+        for (int k = 1; k < Tile::WP; ++k)
+            join_stats(st, joint[k * Tile::kQ + q], heat.log2);
         part[(int64_t)tp * stride + q0 + q] = make_float2(st.m, st.s);
     }
 }
 
-// The rows' losses and stats from the tiles': 16 rows a workgroup, 16 threads a row.
+// The rows' losses and stats from the tiles': ROWS rows a workgroup.
+template <int ROWS>
 __global__ __launch_bounds__(256) void k_ce_loss(CeRows a, CePacked x, int vocab, int tiles,
                                                  const float2 *part, int64_t stride, Heat heat,
                                                  float *loss, float2 *stats)
 {
-    __shared__ float2 joint[16][16];
-    const int r = threadIdx.x & 15, k = threadIdx.x >> 4;
-    const int64_t row = (int64_t)blockIdx.x * 16 + r;
+    constexpr int K = 256 / ROWS;  // threads of a row
+    __shared__ float2 joint[K][ROWS];
+    const int r = threadIdx.x % ROWS, k = threadIdx.x / ROWS;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + r;
     const int at = row < a.rows ? x.place[row] : -1;
     RowStats st = {-INFINITY, 0.0f, 0.0f};
-    if (at >= 0)
-        for (int i = k; i < tiles; i += 16)
+    if (at >= 0) {
+        constexpr int AHEAD = 4;
+        int i = k;
+        for (; i + (AHEAD - 1) * K < tiles; i += AHEAD * K) {
+            float2 p[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                p[u] = part[(int64_t)(i + u * K) * stride + at];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                join_stats(st, p[u], heat.log2);
+        }
+        for (; i < tiles; i += K)
             join_stats(st, part[(int64_t)i * stride + at], heat.log2);
-    joint[k][r] = make_float2(st.m, st.s);
-    __syncthreads();
+    }
+#pragma unroll
+    for (int to = K / 2; to > 0; to /= 2) {
+        joint[k][r] = make_float2(st.m, st.s);
+        __syncthreads();
+        if (k < to)
+            join_stats(st, joint[k + to][r], heat.log2);
+        __syncthreads();
+    }
     if (k > 0 || row >= a.rows)
         return;
     if (at < 0) {
@@ -203,8 +252,6 @@ __global__ __launch_bounds__(256) void k_ce_loss(CeRows a, CePacked x, int vocab
         stats[row] = make_float2(0.0f, 1.0f);
         return;
     }
-    for (int i = 1; i < 16; ++i)
-        join_stats(st, joint[i][r], heat.log2);
     const int target = a.targets[row];
     const float l = target < vocab ? -log_q(x.at_target[at], st, heat) : NAN;
     loss[row] = (a.weight ? a.weight[row] : 1.0f) * l;
@@ -213,25 +260,29 @@ __global__ __launch_bounds__(256) void k_ce_loss(CeRows a, CePacked x, int vocab
 
 // ---- gradients -------------------------------------------------------------------
 
-// dz of a piece of the vocabulary, [rows][width] in bf16; zero behind the last row (up
-// to the tile's end) and the last of the vocabulary.
-__global__ __launch_bounds__(Logit::kThreads, 1) void k_ce_dlogits(CeWeight w, CeRows a,
-                                                                   CePacked x, Heat heat,
-                                                                   const float2 *stats, int piece0,
-                                                                   int width, u16 *dz, int ld)
+// dz of a piece of the vocabulary, [rows][ld] in bf16; zero behind the last row (up to the
+// tile's end, and a whole step) and the last of the vocabulary.
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dlogits(CeWeight w, CeRows a, CePacked x,
+                                                                  Heat heat, const float2 *stats,
+                                                                  int piece0, int width, u16 *dz,
+                                                                  int ld)
 {
-    __shared__ __align__(16) uint8_t lds[Logit::kLds];
+    __shared__ __align__(16) uint8_t lds[Tile::kLds];
     const int count = *x.count;
-    const int np = (min(width, w.vocab - piece0) + Logit::kP - 1) / Logit::kP, nq = (count + Logit::kQ - 1) / Logit::kQ;
+    const int rows = (count + kStepK - 1) / kStepK * kStepK;
+    const int np = (min(width, w.vocab - piece0) + Tile::kP - 1) / Tile::kP;
+    const int nq = (rows + Tile::kQ - 1) / Tile::kQ;
     if ((int)blockIdx.x >= np * nq)
         return;
     int tp, tq;
     product_tile(blockIdx.x, np, nq, tp, tq);
-    const int p0 = piece0 + tp * Logit::kP, q0 = tq * Logit::kQ;
-    Logit t;
+    const int p0 = piece0 + tp * Tile::kP, q0 = tq * Tile::kQ;
+    Tile t;
     logits(t, lds, w, x, p0, count, q0);
+    const bool whole = p0 + Tile::kP <= w.vocab;
 #pragma unroll
-    for (int j = 0; j < Logit::NQ; ++j) {
+    for (int j = 0; j < Tile::NQ; ++j) {
         const int q = q0 + t.q_of(j);
         const bool in = q < count;
         const int row = in ? x.row[q] : 0;
@@ -242,51 +293,59 @@ __global__ __launch_bounds__(Logit::kThreads, 1) void k_ce_dlogits(CeWeight w, C
             scale = NAN;
         const float base = base_of(st.x);
         const float inv = st.y == 0.0f ? 0.0f : scale / st.y;
-        u16 *to = dz + (int64_t)q * ld + tp * Logit::kP;
+        const bool near = __any((unsigned)(target - p0) < (unsigned)Tile::kP);
 #pragma unroll
-        for (int i = 0; i < Logit::NP; ++i) {
+        for (int i = 0; i < Tile::NP; ++i) {
             float d[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int p = p0 + t.p_of(i) + r;
+            for (int r = 0; r < 4; ++r)
                 d[r] = __builtin_amdgcn_exp2f((t.acc[i][j][r] - base) * heat.log2) * inv;
-                d[r] -= p == target ? scale : 0.0f;
-                d[r] = in && p < w.vocab ? d[r] : 0.0f;
+            if (near) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    d[r] -= p0 + t.p_of(i) + r == target ? scale : 0.0f;
             }
-            *reinterpret_cast<gv2u *>(to + t.p_of(i)) = (gv2u){pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])};
+            if (!whole || q0 + Tile::kQ > count) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    d[r] = in && p0 + t.p_of(i) + r < w.vocab ? d[r] : 0.0f;
+            }
+            t.put(lds, i, j, (gv2u){pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])});
         }
     }
+    t.template flush<false>(lds, dz + (int64_t)q0 * ld + tp * Tile::kP, ld, Tile::kQ, Tile::kP);
 }
-
-using Dx = Product<2, 4, 8, 4, false, true>;
 
 // A part of dx = dz w: the products of a stretch of the piece's vocabulary, added to
 // (or, for the first piece, written as) slab blockIdx.y of fp32 sums.
-__global__ __launch_bounds__(Dx::kThreads, 1) void k_ce_dx(CeWeight w, CePacked x, int piece0,
-                                                           int width, int steps, const u16 *dz, int ld,
-                                                           float *sums, int64_t slab, int add)
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dx(CeWeight w, CePacked x, int piece0,
+                                                             int width, int steps, const u16 *dz,
+                                                             int ld, float *sums, int64_t slab,
+                                                             int add)
 {
-    __shared__ __align__(16) uint8_t lds[Dx::kLds];
+    __shared__ __align__(16) uint8_t lds[Tile::kLds];
     const int count = *x.count;
-    const int np = (w.hidden + Dx::kP - 1) / Dx::kP, nq = (count + Dx::kQ - 1) / Dx::kQ;
+    const int np = (w.hidden + Tile::kP - 1) / Tile::kP, nq = (count + Tile::kQ - 1) / Tile::kQ;
     if ((int)blockIdx.x >= np * nq)
         return;
     int tp, tq;
     product_tile(blockIdx.x, np, nq, tp, tq);
-    const int p0 = tp * Dx::kP, q0 = tq * Dx::kQ;
+    const int p0 = tp * Tile::kP, q0 = tq * Tile::kQ;
     const int v0 = (int)blockIdx.y * steps * kStepK;
     const int have = min(width, w.vocab - piece0) - v0;  // of the stretch's vocabulary
     const int n = max(0, min(steps, (have + kStepK - 1) / kStepK));
-    Dx t;
+    Tile t;
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)(piece0 + v0) * w.ld + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + (int64_t)q0 * ld + v0);
-    t.start(lds, w.ld, w.hidden - p0, ld, Dx::kQ, max(0, have));
+    // dz is zero behind the vocabulary's last
+    t.start(lds, w.ld, w.hidden - p0, ld, Tile::kQ, max(0, have));
     t.run(n, p, kStepK * 2 * (uint32_t)w.ld, q, kStepK * 2);
     float *to = sums + blockIdx.y * slab;
 #pragma unroll
-    for (int j = 0; j < Dx::NQ; ++j)
+    for (int j = 0; j < Tile::NQ; ++j)
 #pragma unroll
-        for (int i = 0; i < Dx::NP; ++i) {
+        for (int i = 0; i < Tile::NP; ++i) {
             const int q1 = q0 + t.q_of(j), p1 = p0 + t.p_of(i);
             if (q1 < count && p1 < w.hidden) {
                 v4f *at = reinterpret_cast<v4f *>(to + (int64_t)q1 * w.hidden + p1);
@@ -295,51 +354,54 @@ __global__ __launch_bounds__(Dx::kThreads, 1) void k_ce_dx(CeWeight w, CePacked 
         }
 }
 
-// dx from the slabs of sums, every row of it
+// dx from the slabs of sums, every row of it: 1024 columns a workgroup
 __global__ __launch_bounds__(256) void k_ce_dx_rows(int64_t rows, int hidden, const int *place,
                                                     const float *sums, int64_t slab, int slabs,
                                                     bf16_t *dx, int64_t ld)
 {
-    const int64_t r = blockIdx.x;
+    const int wide = (hidden + 1023) / 1024;
+    const int64_t r = blockIdx.x / wide;
+    const int c = (int)(blockIdx.x % wide) * 1024 + threadIdx.x * 4;
+    if (c >= hidden)
+        return;
     const int at = place[r];
-    for (int c = threadIdx.x * 4; c < hidden; c += 256 * 4) {
-        v4f v = {0.f, 0.f, 0.f, 0.f};
-        if (at >= 0)
-            for (int s = 0; s < slabs; ++s)
-                v += *reinterpret_cast<const v4f *>(sums + s * slab + (int64_t)at * hidden + c);
-        const float f[4] = {v[0], v[1], v[2], v[3]};
-        store_vec(dx + r * ld + c, f);
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+    if (at >= 0) {
+        const float *from = sums + (int64_t)at * hidden + c;
+#pragma unroll 8
+        for (int s = 0; s < slabs; ++s)
+            v += *reinterpret_cast<const v4f *>(from + s * slab);
     }
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    store_vec(dx + r * ld + c, f);
 }
 
-using Dw = Product<2, 4, 8, 4, false, false>;
-
 // dw = dz^T x of a piece of the vocabulary
-__global__ __launch_bounds__(Dw::kThreads, 1) void k_ce_dw(CeWeight w, CePacked x, int piece0,
-                                                           int width, const u16 *dz, int ld,
-                                                           u16 *dw, int64_t ld_dw)
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dw(CeWeight w, CePacked x, int piece0,
+                                                             int width, const u16 *dz, int ld,
+                                                             u16 *dw, int64_t ld_dw)
 {
-    __shared__ __align__(16) uint8_t lds[Dw::kLds];
-    const int np = (w.hidden + Dw::kP - 1) / Dw::kP;
+    __shared__ __align__(16) uint8_t lds[Tile::kLds];
+    const int np = (w.hidden + Tile::kP - 1) / Tile::kP;
     const int have = min(width, w.vocab - piece0);
-    const int nq = (have + Dw::kQ - 1) / Dw::kQ;
+    const int nq = (have + Tile::kQ - 1) / Tile::kQ;
     int tp, tq;
     product_tile(blockIdx.x, np, nq, tp, tq);
-    const int p0 = tp * Dw::kP, q0 = tq * Dw::kQ;
-    Dw t;
+    const int p0 = tp * Tile::kP, q0 = tq * Tile::kQ;
+    Tile t;
     t.start(lds, x.ld, x.ld - p0, ld, width - q0, kStepK);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(x.x + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + q0);
     t.run((*x.count + kStepK - 1) / kStepK, p, kStepK * 2 * x.ld, q, kStepK * 2 * ld);
 #pragma unroll
-    for (int j = 0; j < Dw::NQ; ++j)
+    for (int j = 0; j < Tile::NQ; ++j)
 #pragma unroll
-        for (int i = 0; i < Dw::NP; ++i) {
-            const int q1 = q0 + t.q_of(j), p1 = p0 + t.p_of(i);
-            if (q1 < have && p1 < w.hidden)
-                *reinterpret_cast<gv2u *>(dw + (int64_t)(piece0 + q1) * ld_dw + p1) =
-                    (gv2u){pack_bf16(t.acc[i][j][0], t.acc[i][j][1]), pack_bf16(t.acc[i][j][2], t.acc[i][j][3])};
-        }
+        for (int i = 0; i < Tile::NP; ++i)
+            t.put(lds, i, j, (gv2u){pack_bf16(t.acc[i][j][0], t.acc[i][j][1]),
+                                    pack_bf16(t.acc[i][j][2], t.acc[i][j][3])});
+    t.template flush<true>(lds, dw + (int64_t)(piece0 + q0) * ld_dw + p0, ld_dw, have - q0,
+                           w.hidden - p0);
 }
 
 // ---- the host's side -------------------------------------------------------------
@@ -377,6 +439,33 @@ CePacked take_packed(Carve &c, int64_t rows, int64_t hidden)
     return x;
 }
 
+int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
+// f(Tiles) with the tiles for this many rows
+struct ManyRows {
+    static constexpr int kGroups = 256;  // of dx's products that fill the chip
+    template <bool P_ALONG, bool Q_ALONG> using Tile = Many<P_ALONG, Q_ALONG>;
+    using Dw = Many<false, false>;
+};
+struct SomeRows {
+    static constexpr int kGroups = 512;
+    template <bool P_ALONG, bool Q_ALONG> using Tile = Some<P_ALONG, Q_ALONG>;
+    using Dw = Some<false, false>;
+};
+struct FewRows {
+    static constexpr int kGroups = 1024;
+    template <bool P_ALONG, bool Q_ALONG> using Tile = Few<P_ALONG, Q_ALONG>;
+    using Dw = Some<false, false>;
+};
+template <class F> auto with_tiles(int64_t rows, F f)
+{
+    if (rows <= 32)
+        return f(FewRows{});
+    if (rows <= 128)
+        return f(SomeRows{});
+    return f(ManyRows{});
+}
+
 struct ForwardPlan {
     CePacked x;
     float2 *part;
@@ -388,7 +477,9 @@ ForwardPlan forward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
     ForwardPlan f;
     Carve c = {static_cast<uint8_t *>(ws)};
     f.x = take_packed(c, rows, hidden);
-    f.tiles = (vocab + Logit::kP - 1) / Logit::kP;
+    with_tiles(rows, [&](auto t) {
+        f.tiles = tiles_of(vocab, decltype(t)::template Tile<true, true>::kP);
+    });
     f.stride = up(rows, 16);
     f.part = c.take<float2>(f.tiles * f.stride);
     f.bytes = c.used;
@@ -402,25 +493,31 @@ struct BackwardPlan {
     int64_t width, ld, pieces, slab, slabs, steps;
     size_t bytes;
 };
+constexpr int kWidthStep = 256;  // a piece's width is a multiple of it: of every tile's
 BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
 {
     BackwardPlan b;
     Carve c = {static_cast<uint8_t *>(ws)};
     b.x = take_packed(c, rows, hidden);
-    // a piece's dz stays in the last-level cache for the two products that read it
-    const int64_t padded = up(rows > 0 ? rows : 1, Logit::kQ), most = up(vocab, Logit::kP);
-    int64_t width = (int64_t(1) << 26) / padded / Logit::kP * Logit::kP;
-    width = width < Logit::kP ? Logit::kP : width < most ? width : most;
-    b.pieces = (vocab + width - 1) / width;
-    b.width = up((vocab + b.pieces - 1) / b.pieces, Logit::kP);
-    b.pieces = (vocab + b.width - 1) / b.width;
+    int64_t padded = 0, tiles = 0, groups = 0;
+    with_tiles(rows, [&](auto t) {
+        using Tile = typename decltype(t)::template Tile<false, true>;
+        padded = up(up(rows > 0 ? rows : 1, kStepK), Tile::kQ);
+        tiles = tiles_of(hidden, Tile::kP) * (padded / Tile::kQ);
+        groups = decltype(t)::kGroups;
+    });
+    // pieces of up to 64 Mi logits: 128 MiB of dz
+    const int64_t most = up(vocab, kWidthStep);
+    int64_t width = (int64_t(1) << 26) / padded / kWidthStep * kWidthStep;
+    width = width < kWidthStep ? kWidthStep : width < most ? width : most;
+    b.width = up(tiles_of(vocab, tiles_of(vocab, width)), kWidthStep);
+    b.pieces = tiles_of(vocab, b.width);
     b.ld = pitch(b.width);
     b.dz = c.take<u16>(padded * b.ld);
     // the vocabulary in stretches until the products for dx fill the chip
-    const int64_t tiles = (hidden + Dx::kP - 1) / Dx::kP * (padded / Dx::kQ);
     const int64_t room = b.width / 512 > 0 ? b.width / 512 : 1;
-    b.slabs = tiles >= 256 ? 1 : 256 / tiles < room ? 256 / tiles : room;
-    b.steps = (b.width / kStepK + b.slabs - 1) / b.slabs;
+    b.slabs = tiles >= groups ? 1 : groups / tiles < room ? groups / tiles : room;
+    b.steps = tiles_of(b.width / kStepK, b.slabs);
     b.slab = rows * hidden;
     b.sums = c.take<float>(b.slab * b.slabs);
     b.bytes = c.used;
@@ -450,13 +547,14 @@ mxq_status check(const void *x, int64_t ld_x, const void *w, int64_t ld_w, int64
 }
 
 void launch_pack(const CeRows &a, const void *x, int64_t ld, int64_t hidden, const CePacked &to,
-                 hipStream_t s)
+                 bool zeros, hipStream_t s)
 {
-    // 16 rows a workgroup, more where counting the rows in front would cost more than that
-    const int64_t per = up(a.rows / 1024 < 16 ? 16 : a.rows / 1024, 16);
-    const int64_t groups = a.rows > 0 ? (a.rows + per - 1) / per : 1;
-    hipLaunchKernelGGL(k_ce_pack, dim3((unsigned)groups), dim3(kPackThreads), 0, s, a, per,
-                       static_cast<const bf16_t *>(x), ld, (int)hidden, to);
+    // about 1024 workgroups: more would read the rows in front of their own more often
+    const int64_t per = a.rows > 1024 ? tiles_of(a.rows, 1024) : 1;
+    const int groups = (int)(a.rows > 0 ? tiles_of(a.rows, per) : 1);
+    hipLaunchKernelGGL(k_ce_pack, dim3((unsigned)(groups + (zeros ? kStepK - 1 : 0))),
+                       dim3(kPackThreads), 0, s, a, per, groups, static_cast<const bf16_t *>(x), ld,
+                       (int)hidden, to);
 }
 
 }  // namespace
@@ -494,20 +592,31 @@ extern "C" mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const v
     const ForwardPlan f = forward_plan(rows, hidden, vocab, workspace);
     if (!workspace || ws_bytes < f.bytes)
         return MXQ_ERR_WORKSPACE;
-    const int64_t groups = f.tiles * ((rows + Logit::kQ - 1) / Logit::kQ);
-    if (groups > INT32_MAX)
-        return MXQ_ERR_SHAPE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const CeRows a = {targets, weight, rows};
     const CeWeight cw = {static_cast<const u16 *>(w), ld_w, (int)vocab, (int)hidden};
     const Heat heat = heat_of(temperature);
-    launch_pack(a, x, ld_x, hidden, f.x, s);
-    hipLaunchKernelGGL(k_ce_stats, dim3((unsigned)groups), dim3(Logit::kThreads), 0, s, cw, a, f.x,
-                       heat, f.part, f.stride);
-    hipLaunchKernelGGL(k_ce_loss, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s, a, f.x,
-                       (int)vocab, (int)f.tiles, f.part, f.stride, heat, loss,
-                       reinterpret_cast<float2 *>(stats));
-    return launched();
+    return with_tiles(rows, [&](auto t) {
+        using Tile = typename decltype(t)::template Tile<true, true>;
+        const int64_t groups = f.tiles * tiles_of(rows, Tile::kQ);
+        if (groups > INT32_MAX)
+            return (mxq_status)MXQ_ERR_SHAPE;
+        launch_pack(a, x, ld_x, hidden, f.x, false, s);
+        hipLaunchKernelGGL(k_ce_stats<Tile>, dim3((unsigned)groups), dim3(Tile::kThreads), 0, s, cw,
+                           a, f.x, heat, f.part, f.stride);
+        // 16 rows a workgroup read whole lines; few rows would leave the chip empty
+        const auto loss_of = [&](auto per) {
+            constexpr int ROWS = decltype(per)::value;
+            hipLaunchKernelGGL(k_ce_loss<ROWS>, dim3((unsigned)tiles_of(rows, ROWS)), dim3(256), 0,
+                               s, a, f.x, (int)vocab, (int)f.tiles, f.part, f.stride, heat, loss,
+                               reinterpret_cast<float2 *>(stats));
+        };
+        if (rows <= 512)
+            loss_of(std::integral_constant<int, 1>{});
+        else
+            loss_of(std::integral_constant<int, 16>{});
+        return launched();
+    });
 }
 
 extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const void *w,
@@ -534,37 +643,44 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
     const BackwardPlan b = backward_plan(rows, hidden, vocab, workspace);
     if (!workspace || ws_bytes < b.bytes)
         return MXQ_ERR_WORKSPACE;
-    const int64_t nq = (rows + Logit::kQ - 1) / Logit::kQ;
-    const int64_t z_groups = b.width / Logit::kP * nq;
-    const int64_t x_tiles = (hidden + Dx::kP - 1) / Dx::kP * nq;
-    if (z_groups > INT32_MAX || x_tiles > INT32_MAX)
-        return MXQ_ERR_SHAPE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const CeRows a = {targets, weight, rows};
     const CeWeight cw = {static_cast<const u16 *>(w), ld_w, (int)vocab, (int)hidden};
     const Heat heat = heat_of(temperature);
-    launch_pack(a, x, ld_x, hidden, b.x, s);
-    for (int64_t i = 0; i < b.pieces; ++i) {
-        const int piece0 = (int)(i * b.width);
-        const int64_t have = vocab - piece0 < b.width ? vocab - piece0 : b.width;
-        const int64_t w_tiles = (hidden + Dw::kP - 1) / Dw::kP * ((have + Dw::kQ - 1) / Dw::kQ);
-        if (rows > 0) {
-            const int64_t np = (have + Logit::kP - 1) / Logit::kP;
-            hipLaunchKernelGGL(k_ce_dlogits, dim3((unsigned)(np * nq)), dim3(Logit::kThreads), 0, s,
-                               cw, a, b.x, heat, reinterpret_cast<const float2 *>(stats), piece0,
-                               (int)b.width, b.dz, (int)b.ld);
-            if (dx)
-                hipLaunchKernelGGL(k_ce_dx, dim3((unsigned)x_tiles, (unsigned)b.slabs),
-                                   dim3(Dx::kThreads), 0, s, cw, b.x, piece0, (int)b.width,
-                                   (int)b.steps, b.dz, (int)b.ld, b.sums, b.slab, i > 0);
+    return with_tiles(rows, [&](auto t) {
+        using Logit = typename decltype(t)::template Tile<true, true>;
+        using Dx = typename decltype(t)::template Tile<false, true>;
+        using Dw = typename decltype(t)::Dw;
+        const int64_t nq = tiles_of(rows, Dx::kQ), z_nq = tiles_of(up(rows, kStepK), Logit::kQ);
+        const int64_t x_tiles = tiles_of(hidden, Dx::kP) * nq;
+        if (b.width / Logit::kP * z_nq > INT32_MAX || x_tiles > INT32_MAX ||
+            tiles_of(hidden, 1024) * rows > INT32_MAX)
+            return (mxq_status)MXQ_ERR_SHAPE;
+        launch_pack(a, x, ld_x, hidden, b.x, true, s);
+        for (int64_t i = 0; i < b.pieces; ++i) {
+            const int piece0 = (int)(i * b.width);
+            const int64_t have = vocab - piece0 < b.width ? vocab - piece0 : b.width;
+            if (rows > 0) {
+                hipLaunchKernelGGL(k_ce_dlogits<Logit>,
+                                   dim3((unsigned)(tiles_of(have, Logit::kP) * z_nq)),
+                                   dim3(Logit::kThreads), 0, s, cw, a, b.x, heat,
+                                   reinterpret_cast<const float2 *>(stats), piece0, (int)b.width,
+                                   b.dz, (int)b.ld);
+                if (dx)
+                    hipLaunchKernelGGL(k_ce_dx<Dx>, dim3((unsigned)x_tiles, (unsigned)b.slabs),
+                                       dim3(Dx::kThreads), 0, s, cw, b.x, piece0, (int)b.width,
+                                       (int)b.steps, b.dz, (int)b.ld, b.sums, b.slab, i > 0);
+            }
+            if (dw)
+                hipLaunchKernelGGL(k_ce_dw<Dw>,
+                                   dim3((unsigned)(tiles_of(hidden, Dw::kP) * tiles_of(have, Dw::kQ))),
+                                   dim3(Dw::kThreads), 0, s, cw, b.x, piece0, (int)b.width, b.dz,
+                                   (int)b.ld, static_cast<u16 *>(dw), ld_dw);
         }
-        if (dw)
-            hipLaunchKernelGGL(k_ce_dw, dim3((unsigned)w_tiles), dim3(Dw::kThreads), 0, s, cw, b.x,
-                               piece0, (int)b.width, b.dz, (int)b.ld, static_cast<u16 *>(dw), ld_dw);
-    }
-    if (dx && rows > 0)
-        hipLaunchKernelGGL(k_ce_dx_rows, dim3((unsigned)rows), dim3(256), 0, s, rows, (int)hidden,
-                           b.x.place, b.sums, b.slab, (int)b.slabs, static_cast<bf16_t *>(dx),
-                           ld_dx);
-    return launched();
+        if (dx && rows > 0)
+            hipLaunchKernelGGL(k_ce_dx_rows, dim3((unsigned)(rows * tiles_of(hidden, 1024))),
+                               dim3(256), 0, s, rows, (int)hidden, b.x.place, b.sums, b.slab,
+                               (int)b.slabs, static_cast<bf16_t *>(dx), ld_dx);
+        return launched();
+    });
 }

@@ -293,6 +293,40 @@ template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct
         __builtin_amdgcn_s_waitcnt(0x0070);
         barrier_no_fence();
     }
+    // The tile in bf16 through the LDS, so that it leaves as whole lines: put() every
+    // acc[i][j], packed, then flush().  16-byte chunk c of row q lies at c ^ (q & 15).
+    static_assert(kP * kQ * 2 <= kLds, "the tile in bf16 fits where its operands were");
+    __device__ __forceinline__ void put(uint8_t *lds, int i, int j, gv2u packed) const
+    {
+        const int p = p_of(i), q = q_of(j);
+        typedef __attribute__((address_space(3))) gv2u lds_gv2u;
+        *(lds_gv2u *)(__attribute__((address_space(3))) uint8_t *)(
+            lds + q * (kP * 2) + ((p >> 3) ^ (q & 15)) * 16 + (p & 4) * 2) = packed;
+    }
+    // its first `rows` rows of q and `cols` (a multiple of 8) of p; ONCE: not read again
+    template <bool ONCE>
+    __device__ __forceinline__ void flush(const uint8_t *lds, uint16_t *to, int64_t ld, int rows,
+                                          int cols) const
+    {
+        __syncthreads();
+        constexpr int WIDE = kP / 8;  // chunks of a row
+        const int c = threadIdx.x % WIDE;
+        if (c * 8 >= cols)
+            return;
+#pragma unroll 4
+        for (int q = threadIdx.x / WIDE; q < kQ; q += kThreads / WIDE) {
+            typedef __attribute__((address_space(3))) const gv4u lds_gv4u;
+            const gv4u v = *(lds_gv4u *)(__attribute__((address_space(3))) const uint8_t *)(
+                lds + q * (kP * 2) + (c ^ (q & 15)) * 16);
+            if (q < rows) {
+                MXQ_GLOBAL gv4u *at = (MXQ_GLOBAL gv4u *)(to + (int64_t)q * ld + c * 8);
+                if constexpr (ONCE)
+                    __builtin_nontemporal_store(v, at);
+                else
+                    *at = v;
+            }
+        }
+    }
     // p of acc[i][.][0] and q of acc[.][j] within the tile
     __device__ __forceinline__ int p_of(int i) const { return 16 * (wp + WP * i) + 4 * (lane >> 4); }
     __device__ __forceinline__ int q_of(int j) const { return 16 * (wq + WQ * j) + (lane & 15); }
