@@ -48,18 +48,30 @@ __device__ __forceinline__ void dma16_so(const uint8_t *base, uint32_t off, cons
                  : "memory");
 }
 
-// The same to an LDS address held in a scalar register.
+// The same to an LDS address held in a scalar register.  ONCE: what is not read again leaves
+// the caches to what is.
+template <bool ONCE>
 __device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds)
 {
     uint32_t saved;
-    asm volatile("s_mov_b32 %0, m0\n\t"
-                 "s_mov_b32 m0, %3\n\t"
-                 "s_nop 0\n\t"
-                 "global_load_lds_dwordx4 %1, %2\n\t"
-                 "s_mov_b32 m0, %0"
-                 : "=&s"(saved)
-                 : "v"(off), "s"(base), "s"(lds)
-                 : "memory");
+    if constexpr (ONCE)
+        asm volatile("s_mov_b32 %0, m0\n\t"
+                     "s_mov_b32 m0, %3\n\t"
+                     "s_nop 0\n\t"
+                     "global_load_lds_dwordx4 %1, %2 nt\n\t"
+                     "s_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "v"(off), "s"(base), "s"(lds)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 %0, m0\n\t"
+                     "s_mov_b32 m0, %3\n\t"
+                     "s_nop 0\n\t"
+                     "global_load_lds_dwordx4 %1, %2\n\t"
+                     "s_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "v"(off), "s"(base), "s"(lds)
+                     : "memory");
 }
 
 __device__ __forceinline__ void wait_all_vm()

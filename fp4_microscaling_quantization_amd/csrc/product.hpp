@@ -122,19 +122,38 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
     return reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo);
 }
 
-// A workgroup of WP x WQ waves, each with NP x NQ tiles of 16 x 16.
-template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct Product {
+// A workgroup of WP x WQ waves, each with NP x NQ tiles of 16 x 16, and SLOTS steps in LDS
+// (1: there is one step only).  P_ONCE: P is not read again.
+template <int WP_, int WQ_, int NP_, int NQ_, int SLOTS, bool P_ALONG, bool Q_ALONG,
+          bool P_ONCE = false>
+struct Product {
     static constexpr int WP = WP_, WQ = WQ_, NP = NP_, NQ = NQ_;
     static constexpr int kP = 16 * WP * NP, kQ = 16 * WQ * NQ, kWaves = WP * WQ;
     static constexpr int kThreads = 64 * kWaves;
     using SideP = Side<kP, P_ALONG>;
     using SideQ = Side<kQ, Q_ALONG>;
-    static constexpr int kLds = 2 * (SideP::kBytes + SideQ::kBytes);
+    static constexpr int kLds = SLOTS * (SideP::kBytes + SideQ::kBytes);
     static constexpr int kPerP = SideP::kChunks / kWaves, kPerQ = SideQ::kChunks / kWaves;
     static constexpr int kPer = kPerP + kPerQ;
     static_assert(kPerP * kWaves == SideP::kChunks && kPerQ * kWaves == SideQ::kChunks,
                   "copies split evenly");
-    static_assert(kPer < 16, "a wait counts a step's copies in four bits");
+    static_assert((SLOTS - 1) * kPer < 64, "a wait counts up to 63 copies");
+    // waits for the wave's LDS reads, and until at most N of its copies are still in flight
+    template <int N> static __device__ __forceinline__ void wait()
+    {
+        __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);
+    }
+
+    // the first of `left` <= N steps that are fetched has landed
+    template <int N> static __device__ __forceinline__ void wait_behind(int left)
+    {
+        if constexpr (N <= 1)
+            wait<0>();
+        else if (left >= N)
+            wait<(N - 1) * kPer>();
+        else
+            wait_behind<N - 1>(left);
+    }
 
     v4f acc[NP][NQ];
     int lane, wave, wp, wq;
@@ -146,20 +165,24 @@ template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct
     int cut_step;
     uint32_t cut_p[kPerP];
 
-    // lds: the workgroup's; p, q: leading dimensions and how many rows there are from the
-    // tile's first; k: how many there are of it
-    __device__ __forceinline__ void start(uint8_t *lds, int64_t ldp, int have_p, int64_t ldq,
-                                          int have_q, int k)
+    __device__ __forceinline__ void place()
     {
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         wp = wave % WP;
         wq = wave / WP;
+    }
+    // lds: the workgroup's; p, q: leading dimensions and how many rows there are from the
+    // tile's first; k: how many there are of it
+    __device__ __forceinline__ void start(uint8_t *lds, int64_t ldp, int have_p, int64_t ldq,
+                                          int have_q, int k)
+    {
+        place();
         const uint32_t l = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t *)lds);
         read_p.start(l, wp, lane);
-        read_q.start(l + 2 * SideP::kBytes, wq, lane);
+        read_q.start(l + SLOTS * SideP::kBytes, wq, lane);
         at_p = __builtin_amdgcn_readfirstlane(l + wave * 1024);
-        at_q = __builtin_amdgcn_readfirstlane(l + 2 * SideP::kBytes + wave * 1024);
+        at_q = __builtin_amdgcn_readfirstlane(l + SLOTS * SideP::kBytes + wave * 1024);
         cut_step = k % kStepK ? k / kStepK : -1;
         const int left = k % kStepK ? k % kStepK : kStepK;
 #pragma unroll
@@ -180,10 +203,10 @@ template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct
     __device__ __forceinline__ void copy(int n, int s, int slot, const uint8_t *p, const uint8_t *q)
     {
         if (n < kPerP)
-            copy16(p, s == cut_step ? cut_p[n] : off_p[n],
+            copy16<P_ONCE>(p, s == cut_step ? cut_p[n] : off_p[n],
                    at_p + slot * SideP::kBytes + n * (kWaves * 1024));
         else
-            copy16(q, off_q[n - kPerP],
+            copy16<false>(q, off_q[n - kPerP],
                    at_q + slot * SideQ::kBytes + (n - kPerP) * (kWaves * 1024));
     }
     // fragment n of a half: P's first, all of Q's, the rest of P's
@@ -218,65 +241,70 @@ template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct
     // `steps` steps from the (uniform) addresses p and q of the first one's tiles, each
     // dp and dq bytes further.  All of the LDS is free again when it returns.
     //
-    // Two slots.  Each half's fragments are read during the half before it, so a step's
-    // slot has been read when its first half is done: there, once a step, is the barrier,
-    // and the step after the next is fetched behind it into the same slot.  It lands
-    // during the second half and the next step's first one.
+    // Each half's fragments are read during the half before it, so a step's slot has been
+    // read when its first half is done: there, once a step, is the barrier, and the step
+    // SLOTS further is fetched behind it into the same slot.  With two slots it lands during
+    // the second half and the next step's first one.
     // The steps are taken in a circle from step `first`.
     __device__ __forceinline__ void run(int steps, const uint8_t *p, uint32_t dp, const uint8_t *q,
                                         uint32_t dq, int first = 0)
     {
         if (steps <= 0)
             return;
-        steps = __builtin_amdgcn_readfirstlane(steps);
+        steps = SLOTS == 1 ? 1 : __builtin_amdgcn_readfirstlane(steps);
         p = uniform(p);
         q = uniform(q);
         int at = __builtin_amdgcn_readfirstlane(first);  // the step that is fetched next
         const auto next = [&] { at = at + 1 < steps ? at + 1 : 0; };
 #pragma unroll
-        for (int n = 0; n < kPer; ++n)
-            copy(n, at, 0, p + (uint64_t)(uint32_t)at * dp, q + (uint64_t)(uint32_t)at * dq);
-        next();
-        if (steps > 1) {
+        for (int i = 0; i < SLOTS; ++i)
+            if (i < steps) {
 #pragma unroll
-            for (int n = 0; n < kPer; ++n)
-                copy(n, at, 1, p + (uint64_t)(uint32_t)at * dp, q + (uint64_t)(uint32_t)at * dq);
-            next();
-            __builtin_amdgcn_s_waitcnt(0x0070 | kPer);
-        } else {
-            __builtin_amdgcn_s_waitcnt(0x0070);
-        }
+                for (int n = 0; n < kPer; ++n)
+                    copy(n, at, i, p + (uint64_t)(uint32_t)at * dp, q + (uint64_t)(uint32_t)at * dq);
+                next();
+            }
+        // of `left` steps that are fetched, the first has landed
+        const auto landed = [&](int left) { wait_behind<SLOTS>(left); };
+        landed(min(steps, SLOTS));
         barrier_no_fence();
         v8bf fp[2][NP], fq[2][NQ];
         constexpr int FRAGMENTS = NP + NQ;
 #pragma unroll
         for (int n = 0; n < FRAGMENTS; ++n)
             fragment(n, 0, fp[0], fq[0]);
-        const auto step = [&](int s, auto copies, auto last) {
+        int slot = 0;
+        const auto step = [&](int left, auto copies, auto last) {  // left: steps from this one on
             constexpr bool COPY = decltype(copies)::value, LAST = decltype(last)::value;
-            const int slot = s & 1;
             __builtin_amdgcn_sched_barrier(0);
             products<FRAGMENTS>(fp[0], fq[0], [&](int n) { fragment(n, 1, fp[1], fq[1]); });
             if constexpr (LAST) {
                 products<0>(fp[1], fq[1], [](int) {});
             } else {
-                // this wave's copies of step s + 1 have landed, its reads of step s are done ...
-                __builtin_amdgcn_s_waitcnt(0x0070);
+                // this wave's copies of the next step have landed, its reads of this one are
+                // done ...
+                if constexpr (COPY)
+                    wait<(SLOTS > 2 ? SLOTS - 2 : 0) * kPer>();
+                else
+                    landed(left - 1);
                 // ... and everyone's
                 barrier_no_fence();
                 __builtin_amdgcn_sched_barrier(0);
-                read_p.move(slot ? -SideP::kBytes : SideP::kBytes);
-                read_q.move(slot ? -SideQ::kBytes : SideQ::kBytes);
+                const int behind = slot + 1 < SLOTS ? 1 : 1 - SLOTS;
+                read_p.move(behind * SideP::kBytes);
+                read_q.move(behind * SideQ::kBytes);
                 const uint8_t *ps = p + (uint64_t)(uint32_t)at * dp;
                 const uint8_t *qs = q + (uint64_t)(uint32_t)at * dq;
                 constexpr int COPIES = COPY ? kPer : 0;
                 products<FRAGMENTS + COPIES>(fp[1], fq[1], [&](int n) {
                     // a copy and a fragment in turn, copies first: they take longest
-                    if (n < 2 * COPIES ? n % 2 == 0 : false)
-                        copy(n / 2, at, slot, ps, qs);
+                    constexpr int TURNS = COPIES < FRAGMENTS ? COPIES : FRAGMENTS;
+                    if (n < 2 * TURNS ? n % 2 == 0 : COPIES > FRAGMENTS)
+                        copy(n < 2 * TURNS ? n / 2 : n - TURNS, at, slot, ps, qs);
                     else
-                        fragment(n < 2 * COPIES ? n / 2 : n - COPIES, 0, fp[0], fq[0]);
+                        fragment(n < 2 * TURNS ? n / 2 : n - TURNS, 0, fp[0], fq[0]);
                 });
+                slot += behind;
                 if constexpr (COPY)
                     next();
             }
@@ -284,13 +312,15 @@ template <int WP_, int WQ_, int NP_, int NQ_, bool P_ALONG, bool Q_ALONG> struct
         constexpr std::true_type yes{};
         constexpr std::false_type no{};
         int s = 0;
-        for (; s + 2 < steps; ++s)
-            step(s, yes, no);
-        if (steps > 1)
-            step(s++, no, no);
-        step(s, no, yes);
+        if constexpr (SLOTS > 1) {
+            for (; s + SLOTS < steps; ++s)
+                step(0, yes, no);
+            for (; s + 1 < steps; ++s)
+                step(steps - s, no, no);
+        }
+        step(1, no, yes);
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0x0070);
+        wait<0>();
         barrier_no_fence();
     }
     // The tile in bf16 through the LDS, so that it leaves as whole lines: put() every
