@@ -120,16 +120,19 @@ __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per,
 
 // ---- logits ----------------------------------------------------------------------
 
-// Tiles for many rows, and for few, where the weight is what there is to read: one wave
-// wide in the rows, several workgroups a CU.
+// Tiles, p x q.  Many: for products that fill the chip with them.
 template <bool P_ALONG, bool Q_ALONG> using Many = Product<2, 4, 8, 4, 2, P_ALONG, Q_ALONG>;  // 256 x 256
-template <bool P_ALONG, bool Q_ALONG> using Some = Product<4, 1, 2, 8, 2, P_ALONG, Q_ALONG>;  // 128 x 128
-template <bool P_ALONG, bool Q_ALONG> using Few = Product<4, 1, 2, 2, 4, P_ALONG, Q_ALONG>;   // 128 x 32
-
-// (24 x 4096 x 128256 in the forward pass 205 us without the hint, 182 with it)
-using FewOnce = Product<4, 1, 2, 2, 4, true, true, true>;
-using SomeOnce = Product<4, 1, 2, 8, 2, true, true, true>;
-// for dw of rows that are one step of the product over them
+// For those that do not: half as large, and a step more in flight.
+template <bool P_ALONG, bool Q_ALONG> using Half = Product<2, 4, 4, 4, 3, P_ALONG, Q_ALONG>;  // 128 x 256
+// A quarter: one to a CU with four steps in LDS, two with two.
+template <bool P_ALONG, bool Q_ALONG, bool ONCE = false>
+using Deep = Product<4, 2, 2, 4, 4, P_ALONG, Q_ALONG, ONCE>;  // 128 x 128
+template <bool P_ALONG, bool Q_ALONG, bool ONCE = false>
+using Twin = Product<4, 1, 2, 8, 2, P_ALONG, Q_ALONG, ONCE>;  // 128 x 128
+// Few rows, where the weight is what there is to read
+template <bool P_ALONG, bool Q_ALONG, bool ONCE = false>
+using Few = Product<4, 1, 2, 2, 4, P_ALONG, Q_ALONG, ONCE>;  // 128 x 32
+// dw of rows that are one step of the product over them
 using Outer = Product<2, 2, 4, 4, 1, false, false>;  // 128 x 128
 
 // the tile's product: w rows from p0, packed x rows from q0
@@ -456,40 +459,48 @@ CePacked take_packed(Carve &c, int64_t rows, int64_t hidden)
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 
-// f(Tiles) with the tiles for this many rows
-struct ManyRows {
-    static constexpr int kGroups = 256;  // of dx's products that fill the chip
-    using Stats = Many<true, true>;
-    template <bool P_ALONG, bool Q_ALONG> using Tile = Many<P_ALONG, Q_ALONG>;
-    using Dw = Many<false, false>;
+template <class T> struct Tag {
+    using Tile = T;
 };
-struct SomeRows {
-    static constexpr int kGroups = 512;
-    using Stats = SomeOnce;
-    template <bool P_ALONG, bool Q_ALONG> using Tile = Some<P_ALONG, Q_ALONG>;
-    using Dw = Some<false, false>;
-};
-struct StepRows {  // one step of the product over them
-    static constexpr int kGroups = 512;
-    using Stats = SomeOnce;
-    template <bool P_ALONG, bool Q_ALONG> using Tile = Some<P_ALONG, Q_ALONG>;
-    using Dw = Outer;
-};
-struct FewRows {
-    static constexpr int kGroups = 1024;
-    using Stats = FewOnce;
-    template <bool P_ALONG, bool Q_ALONG> using Tile = Few<P_ALONG, Q_ALONG>;
-    using Dw = Outer;
-};
-template <class F> auto with_tiles(int64_t rows, F f)
+constexpr int kCus = 256;
+
+// f(Tag<Tile>) for the logits of a stretch of the vocabulary.  ONCE: its weight is read by
+// nobody else soon; where all rows are one tile, it then leaves the caches to what is (24 x
+// 4096 x 128256 in the forward pass 205 us without the hint, 182 with it).
+template <bool ONCE, class F> auto with_logits(int64_t rows, int64_t vocab, F f)
 {
     if (rows <= 32)
-        return f(FewRows{});
-    if (rows <= kStepK)
-        return f(StepRows{});
+        return f(Tag<Few<true, true, ONCE>>{});
+    // 100 rows under 32000 x 4096 (250 tiles) Deep 64 us, Twin 78; under 128256 x 4096 222 and 203
+    if (rows <= 128) {
+        if (tiles_of(vocab, 128) <= kCus)
+            return f(Tag<Deep<true, true, ONCE>>{});
+        return f(Tag<Twin<true, true, ONCE>>{});
+    }
+    // 200 rows under 32000 x 4096 (125 tiles) Half 79 us, Many 126; 400 rows (250) 153 and 135
+    if (tiles_of(vocab, 256) * tiles_of(rows, 256) <= kCus / 2)
+        return f(Tag<Half<true, true>>{});
+    return f(Tag<Many<true, true>>{});
+}
+// for dx, whose tiles are made enough by stretches of the vocabulary
+template <class F> auto with_dx(int64_t rows, F f)
+{
+    if (rows <= 32)
+        return f(Tag<Few<false, true>>{});
     if (rows <= 128)
-        return f(SomeRows{});
-    return f(ManyRows{});
+        return f(Tag<Twin<false, true>>{});
+    return f(Tag<Many<false, true>>{});
+}
+// for dw
+template <class F> auto with_dw(int64_t rows, int64_t hidden, int64_t vocab, F f)
+{
+    if (rows <= kStepK)
+        return f(Tag<Outer>{});
+    if (tiles_of(vocab, 256) * tiles_of(hidden, 256) <= kCus / 2)
+        return f(Tag<Deep<false, false>>{});
+    if (rows <= 2 * kStepK)
+        return f(Tag<Twin<false, false>>{});
+    return f(Tag<Many<false, false>>{});
 }
 
 struct ForwardPlan {
@@ -503,8 +514,8 @@ ForwardPlan forward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
     ForwardPlan f;
     Carve c = {static_cast<uint8_t *>(ws)};
     f.x = take_packed(c, rows, hidden);
-    with_tiles(rows, [&](auto t) {
-        f.tiles = tiles_of(vocab, decltype(t)::Stats::kP);
+    with_logits<true>(rows, vocab, [&](auto t) {
+        f.tiles = tiles_of(vocab, decltype(t)::Tile::kP);
     });
     f.stride = up(rows, 16);
     f.part = c.take<float2>(f.tiles * f.stride);
@@ -519,19 +530,14 @@ struct BackwardPlan {
     int64_t width, ld, pieces, slab, slabs, steps;
     size_t bytes;
 };
-constexpr int kWidthStep = 256;  // a piece's width is a multiple of it: of every tile's
+// a piece's width is a multiple of it, and so is how many rows dz has: of every tile's
+constexpr int kWidthStep = 256, kRowStep = 256;
 BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
 {
     BackwardPlan b;
     Carve c = {static_cast<uint8_t *>(ws)};
     b.x = take_packed(c, rows, hidden);
-    int64_t padded = 0, tiles = 0, groups = 0;
-    with_tiles(rows, [&](auto t) {
-        using Tile = typename decltype(t)::template Tile<false, true>;
-        padded = up(up(rows > 0 ? rows : 1, kStepK), Tile::kQ);
-        tiles = tiles_of(hidden, Tile::kP) * (padded / Tile::kQ);
-        groups = decltype(t)::kGroups;
-    });
+    const int64_t padded = up(rows > 0 ? rows : 1, kRowStep);
     // Pieces of up to 64 Mi logits: 128 MiB of dz.  (Pieces whose weight stays in the
     // last-level cache leave CUs idle with few rows: 100 x 4096 x 128256 in pieces of 16384
     // 1123 us, in one 737.)
@@ -544,7 +550,12 @@ BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws
     b.dz = c.take<u16>(padded * b.ld);
     // the vocabulary in stretches until the products for dx fill the chip
     const int64_t room = b.width / 512 > 0 ? b.width / 512 : 1;
-    b.slabs = tiles >= groups ? 1 : groups / tiles < room ? groups / tiles : room;
+    with_dx(rows, [&](auto t) {
+        using Tile = typename decltype(t)::Tile;
+        const int64_t tiles = tiles_of(hidden, Tile::kP) * tiles_of(rows > 0 ? rows : 1, Tile::kQ);
+        const int64_t groups = kCus * (Tile::kLds <= 65536 ? 2 : 1) * (rows <= 32 ? 2 : 1);
+        b.slabs = tiles >= groups ? 1 : groups / tiles < room ? groups / tiles : room;
+    });
     b.steps = tiles_of(b.width / kStepK, b.slabs);
     b.slab = rows * hidden;
     b.sums = c.take<float>(b.slab * b.slabs);
@@ -624,8 +635,8 @@ extern "C" mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const v
     const CeRows a = {targets, weight, rows};
     const CeWeight cw = {static_cast<const u16 *>(w), ld_w, (int)vocab, (int)hidden};
     const Heat heat = heat_of(temperature);
-    return with_tiles(rows, [&](auto t) {
-        using Tile = typename decltype(t)::Stats;
+    return with_logits<true>(rows, vocab, [&](auto t) {
+        using Tile = typename decltype(t)::Tile;
         const int64_t groups = f.tiles * tiles_of(rows, Tile::kQ);
         if (groups > INT32_MAX)
             return (mxq_status)MXQ_ERR_SHAPE;
@@ -675,40 +686,47 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
     const CeRows a = {targets, weight, rows};
     const CeWeight cw = {static_cast<const u16 *>(w), ld_w, (int)vocab, (int)hidden};
     const Heat heat = heat_of(temperature);
-    return with_tiles(rows, [&](auto t) {
-        using Logit = typename decltype(t)::template Tile<true, true>;
-        using Dx = typename decltype(t)::template Tile<false, true>;
-        using Dw = typename decltype(t)::Dw;
-        const int64_t nq = tiles_of(rows, Dx::kQ);
-        const int64_t x_tiles = tiles_of(hidden, Dx::kP) * nq;
-        if (b.width / Logit::kP * nq > INT32_MAX || x_tiles > INT32_MAX ||
-            tiles_of(hidden, 1024) * rows > INT32_MAX)
-            return (mxq_status)MXQ_ERR_SHAPE;
-        launch_pack(a, x, ld_x, hidden, b.x, true, s);
-        for (int64_t i = 0; i < b.pieces; ++i) {
-            const int piece0 = (int)(i * b.width);
-            const int64_t have = vocab - piece0 < b.width ? vocab - piece0 : b.width;
-            if (rows > 0) {
-                hipLaunchKernelGGL(k_ce_dlogits<Logit>,
-                                   dim3((unsigned)(tiles_of(have, Logit::kP) * nq)),
-                                   dim3(Logit::kThreads), 0, s, cw, a, b.x, heat,
-                                   reinterpret_cast<const float2 *>(stats), piece0, (int)b.width,
-                                   b.dz, (int)b.ld);
-                if (dx)
-                    hipLaunchKernelGGL(k_ce_dx<Dx>, dim3((unsigned)x_tiles, (unsigned)b.slabs),
-                                       dim3(Dx::kThreads), 0, s, cw, b.x, piece0, (int)b.width,
-                                       (int)b.steps, b.dz, (int)b.ld, b.sums, b.slab, i > 0);
-            }
-            if (dw)
-                hipLaunchKernelGGL(k_ce_dw<Dw>,
-                                   dim3((unsigned)(tiles_of(hidden, Dw::kP) * tiles_of(have, Dw::kQ))),
-                                   dim3(Dw::kThreads), 0, s, cw, b.x, piece0, (int)b.width, b.dz,
-                                   (int)b.ld, static_cast<u16 *>(dw), ld_dw);
-        }
-        if (dx && rows > 0)
-            hipLaunchKernelGGL(k_ce_dx_rows, dim3((unsigned)(rows * tiles_of(hidden, 1024))),
-                               dim3(256), 0, s, rows, (int)hidden, b.x.place, b.sums, b.slab,
-                               (int)b.slabs, static_cast<bf16_t *>(dx), ld_dx);
-        return launched();
-    });
+    if (tiles_of(b.width, 128) * tiles_of(rows, 32) > INT32_MAX ||
+        tiles_of(hidden, 128) * tiles_of(rows, 32) > INT32_MAX ||
+        tiles_of(hidden, 128) * tiles_of(b.width, 128) > INT32_MAX ||
+        tiles_of(hidden, 1024) * rows > INT32_MAX)
+        return MXQ_ERR_SHAPE;
+    launch_pack(a, x, ld_x, hidden, b.x, true, s);
+    for (int64_t i = 0; i < b.pieces; ++i) {
+        const int piece0 = (int)(i * b.width);
+        const int64_t have = vocab - piece0 < b.width ? vocab - piece0 : b.width;
+        if (rows > 0)
+            with_logits<false>(rows, b.width, [&](auto t) {
+                using Tile = typename decltype(t)::Tile;
+                hipLaunchKernelGGL(
+                    k_ce_dlogits<Tile>,
+                    dim3((unsigned)(tiles_of(have, Tile::kP) * tiles_of(rows, Tile::kQ))),
+                    dim3(Tile::kThreads), 0, s, cw, a, b.x, heat,
+                    reinterpret_cast<const float2 *>(stats), piece0, (int)b.width, b.dz, (int)b.ld);
+            });
+        if (rows > 0 && dx)
+            with_dx(rows, [&](auto t) {
+                using Tile = typename decltype(t)::Tile;
+                hipLaunchKernelGGL(
+                    k_ce_dx<Tile>,
+                    dim3((unsigned)(tiles_of(hidden, Tile::kP) * tiles_of(rows, Tile::kQ)),
+                         (unsigned)b.slabs),
+                    dim3(Tile::kThreads), 0, s, cw, b.x, piece0, (int)b.width, (int)b.steps, b.dz,
+                    (int)b.ld, b.sums, b.slab, i > 0);
+            });
+        if (dw)
+            with_dw(rows, hidden, b.width, [&](auto t) {
+                using Tile = typename decltype(t)::Tile;
+                hipLaunchKernelGGL(
+                    k_ce_dw<Tile>,
+                    dim3((unsigned)(tiles_of(hidden, Tile::kP) * tiles_of(have, Tile::kQ))),
+                    dim3(Tile::kThreads), 0, s, cw, b.x, piece0, (int)b.width, b.dz, (int)b.ld,
+                    static_cast<u16 *>(dw), ld_dw);
+            });
+    }
+    if (dx && rows > 0)
+        hipLaunchKernelGGL(k_ce_dx_rows, dim3((unsigned)(rows * tiles_of(hidden, 1024))), dim3(256),
+                           0, s, rows, (int)hidden, b.x.place, b.sums, b.slab, (int)b.slabs,
+                           static_cast<bf16_t *>(dx), ld_dx);
+    return launched();
 }
