@@ -269,35 +269,58 @@ __global__ __launch_bounds__(256) void k_ce_loss(CeRows a, CePacked x, int vocab
 
 // ---- gradients -------------------------------------------------------------------
 
-// dz of a piece of the vocabulary, [rows][ld] in bf16; zero behind the last row (up to the
-// tile's end, and a whole step) and the last of the vocabulary.
-template <class Tile>
-__global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dlogits(CeWeight w, CeRows a, CePacked x,
-                                                                  Heat heat, const float2 *stats,
-                                                                  int piece0, int width, u16 *dz,
-                                                                  int ld)
+// The backward pass over pieces of `width` of the vocabulary
+struct Backward {
+    CeWeight w;
+    CeRows a;
+    CePacked x;
+    Heat heat;
+    const float2 *stats;
+    int width, ld;  // of dz
+    u16 *dz;        // of a piece, [rows][ld]
+    float *sums;    // slabs of [count][hidden]
+    int fill, room; // workgroups that fill the chip, and most slabs
+    u16 *dw;
+    int64_t ld_dw;
+
+    __device__ __forceinline__ int first(int piece) const { return piece * width; }
+    __device__ __forceinline__ int have(int piece) const
+    {
+        return min(width, w.vocab - first(piece));
+    }
+};
+
+// The products for dx are split over stretches of a piece's vocabulary until they fill the
+// chip; each stretch has its own slab of sums.  How many rows count is only known here.
+__device__ __forceinline__ int slabs_of(int tiles, int fill, int room)
 {
-    __shared__ __align__(16) uint8_t lds[Tile::kLds];
-    const int count = *x.count;
-    const int np = (min(width, w.vocab - piece0) + Tile::kP - 1) / Tile::kP;
+    return tiles >= fill ? 1 : max(1, min(fill / max(1, tiles), room));
+}
+
+// Tile `at` of the piece's dz, [rows][ld] in bf16; zero behind the last row (up to the
+// tile's end, and a whole step) and the last of the vocabulary.
+template <class Tile> __device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int piece, int at)
+{
+    const int count = *b.x.count;
+    const int np = (b.have(piece) + Tile::kP - 1) / Tile::kP;
     const int nq = (count + Tile::kQ - 1) / Tile::kQ;
-    if ((int)blockIdx.x >= np * nq)
+    if (at >= np * nq)
         return;
     int tp, tq;
-    product_tile(blockIdx.x, np, nq, tp, tq);
-    const int p0 = piece0 + tp * Tile::kP, q0 = tq * Tile::kQ;
+    product_tile(at, np, nq, tp, tq);
+    const int p0 = b.first(piece) + tp * Tile::kP, q0 = tq * Tile::kQ;
     Tile t;
-    logits(t, lds, w, x, p0, count, q0);
-    const bool whole = p0 + Tile::kP <= w.vocab;
+    logits(t, lds, b.w, b.x, p0, count, q0);
+    const bool whole = p0 + Tile::kP <= b.w.vocab;
 #pragma unroll
     for (int j = 0; j < Tile::NQ; ++j) {
         const int q = q0 + t.q_of(j);
         const bool in = q < count;
-        const int row = in ? x.row[q] : 0;
-        const int target = in ? a.targets[row] : -1;
-        const float2 st = in ? stats[row] : make_float2(0.0f, 1.0f);
-        float scale = in ? (a.weight ? a.weight[row] : 1.0f) * heat.inv : 0.0f;
-        if (target >= w.vocab)
+        const int row = in ? b.x.row[q] : 0;
+        const int target = in ? b.a.targets[row] : -1;
+        const float2 st = in ? b.stats[row] : make_float2(0.0f, 1.0f);
+        float scale = in ? (b.a.weight ? b.a.weight[row] : 1.0f) * b.heat.inv : 0.0f;
+        if (target >= b.w.vocab)
             scale = NAN;
         const float base = base_of(st.x);
         const float inv = st.y == 0.0f ? 0.0f : scale / st.y;
@@ -307,7 +330,7 @@ __global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dlogits(CeWeight w, Ce
             float d[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                d[r] = __builtin_amdgcn_exp2f((t.acc[i][j][r] - base) * heat.log2) * inv;
+                d[r] = __builtin_amdgcn_exp2f((t.acc[i][j][r] - base) * b.heat.log2) * inv;
             if (near) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
@@ -316,110 +339,127 @@ __global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dlogits(CeWeight w, Ce
             if (!whole || q0 + Tile::kQ > count) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    d[r] = in && p0 + t.p_of(i) + r < w.vocab ? d[r] : 0.0f;
+                    d[r] = in && p0 + t.p_of(i) + r < b.w.vocab ? d[r] : 0.0f;
             }
             t.put(lds, i, j, (gv2u){pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])});
         }
     }
-    u16 *to = dz + (int64_t)q0 * ld + tp * Tile::kP;
-    t.template flush<false>(lds, to, ld, Tile::kQ, Tile::kP);
+    u16 *to = b.dz + (int64_t)q0 * b.ld + tp * Tile::kP;
+    t.template flush<false>(lds, to, b.ld, Tile::kQ, Tile::kP);
     // what is left of a step behind the last tile
     if constexpr (Tile::kQ < kStepK) {
         constexpr int WIDE = Tile::kP / 8;
         const int rows = (count + kStepK - 1) / kStepK * kStepK;
         if (tq == nq - 1)
             for (int q = Tile::kQ + threadIdx.x / WIDE; q < rows - q0; q += Tile::kThreads / WIDE)
-                *reinterpret_cast<gv4u *>(to + (int64_t)q * ld + threadIdx.x % WIDE * 8) =
+                *reinterpret_cast<gv4u *>(to + (int64_t)q * b.ld + threadIdx.x % WIDE * 8) =
                     (gv4u){0u, 0u, 0u, 0u};
     }
 }
 
-// A part of dx = dz w: the products of a stretch of the piece's vocabulary, added to
-// (or, for the first piece, written as) slab blockIdx.y of fp32 sums.
-template <class Tile>
-__global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dx(CeWeight w, CePacked x, int piece0,
-                                                             int width, int steps, const u16 *dz,
-                                                             int ld, float *sums, int64_t slab,
-                                                             int add)
+// Tile `at` of all slabs' for dx = dz w, added to (for the first piece, written as) the sums.
+template <class Tile> __device__ __forceinline__ void dx_part(uint8_t *lds, const Backward &b, int piece, int at)
 {
-    __shared__ __align__(16) uint8_t lds[Tile::kLds];
-    const int count = *x.count;
-    const int np = (w.hidden + Tile::kP - 1) / Tile::kP, nq = (count + Tile::kQ - 1) / Tile::kQ;
-    if ((int)blockIdx.x >= np * nq)
+    const int count = *b.x.count;
+    const int np = (b.w.hidden + Tile::kP - 1) / Tile::kP, nq = (count + Tile::kQ - 1) / Tile::kQ;
+    const int slabs = slabs_of(np * nq, b.fill, b.room);
+    const int slab = at / max(1, np * nq);
+    if (slab >= slabs || nq == 0)
         return;
+    at -= slab * np * nq;
     int tp, tq;
-    product_tile(blockIdx.x, np, nq, tp, tq);
+    product_tile(at, np, nq, tp, tq);
     const int p0 = tp * Tile::kP, q0 = tq * Tile::kQ;
-    const int v0 = (int)blockIdx.y * steps * kStepK;
-    const int have = min(width, w.vocab - piece0) - v0;  // of the stretch's vocabulary
+    const int steps = (b.width / kStepK + slabs - 1) / slabs;
+    const int v0 = slab * steps * kStepK;
+    const int have = b.have(piece) - v0;  // of the stretch's vocabulary, to the piece's end
     const int n = max(0, min(steps, (have + kStepK - 1) / kStepK));
     Tile t;
-    const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)(piece0 + v0) * w.ld + p0);
-    const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + (int64_t)q0 * ld + v0);
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(b.w.w + (int64_t)(b.first(piece) + v0) * b.w.ld + p0);
+    const uint8_t *q = reinterpret_cast<const uint8_t *>(b.dz + (int64_t)q0 * b.ld + v0);
     // dz is zero behind the vocabulary's last
-    t.start(lds, w.ld, w.hidden - p0, ld, Tile::kQ, max(0, have));
-    t.run(n, p, kStepK * 2 * (uint32_t)w.ld, q, kStepK * 2);
-    float *to = sums + blockIdx.y * slab;
+    t.start(lds, b.w.ld, b.w.hidden - p0, b.ld, Tile::kQ, max(0, have));
+    t.run(n, p, kStepK * 2 * (uint32_t)b.w.ld, q, kStepK * 2);
+    float *to = b.sums + (int64_t)slab * count * b.w.hidden;
 #pragma unroll
     for (int j = 0; j < Tile::NQ; ++j)
 #pragma unroll
         for (int i = 0; i < Tile::NP; ++i) {
             const int q1 = q0 + t.q_of(j), p1 = p0 + t.p_of(i);
-            if (q1 < count && p1 < w.hidden) {
-                v4f *at = reinterpret_cast<v4f *>(to + (int64_t)q1 * w.hidden + p1);
-                *at = add ? *at + t.acc[i][j] : t.acc[i][j];
+            if (q1 < count && p1 < b.w.hidden) {
+                v4f *sum = reinterpret_cast<v4f *>(to + (int64_t)q1 * b.w.hidden + p1);
+                *sum = piece > 0 ? *sum + t.acc[i][j] : t.acc[i][j];
             }
         }
 }
 
-// dx from the slabs of sums, every row of it: 1024 columns a workgroup
-__global__ __launch_bounds__(256) void k_ce_dx_rows(int64_t rows, int hidden, const int *place,
-                                                    const float *sums, int64_t slab, int slabs,
-                                                    bf16_t *dx, int64_t ld)
+// Tile `at` of dw = dz^T x of the piece's vocabulary.
+template <class Tile> __device__ __forceinline__ void dw_part(uint8_t *lds, const Backward &b, int piece, int at)
 {
-    const int wide = (hidden + 1023) / 1024;
-    const int64_t r = blockIdx.x / wide;
-    const int c = (int)(blockIdx.x % wide) * 1024 + threadIdx.x * 4;
-    if (c >= hidden)
-        return;
-    const int at = place[r];
-    v4f v = {0.f, 0.f, 0.f, 0.f};
-    if (at >= 0) {
-        const float *from = sums + (int64_t)at * hidden + c;
-#pragma unroll 8
-        for (int s = 0; s < slabs; ++s)
-            v += *reinterpret_cast<const v4f *>(from + s * slab);
-    }
-    const float f[4] = {v[0], v[1], v[2], v[3]};
-    store_vec(dx + r * ld + c, f);
-}
-
-// dw = dz^T x of a piece of the vocabulary
-template <class Tile>
-__global__ __launch_bounds__(Tile::kThreads, Tile::kLds <= 32768 ? 4 : 1) void k_ce_dw(CeWeight w, CePacked x, int piece0,
-                                                             int width, const u16 *dz, int ld,
-                                                             u16 *dw, int64_t ld_dw)
-{
-    __shared__ __align__(16) uint8_t lds[Tile::kLds];
-    const int np = (w.hidden + Tile::kP - 1) / Tile::kP;
-    const int have = min(width, w.vocab - piece0);
+    const int np = (b.w.hidden + Tile::kP - 1) / Tile::kP;
+    const int have = b.have(piece);
     const int nq = (have + Tile::kQ - 1) / Tile::kQ;
+    if (at >= np * nq)
+        return;
     int tp, tq;
-    product_tile(blockIdx.x, np, nq, tp, tq);
+    product_tile(at, np, nq, tp, tq);
     const int p0 = tp * Tile::kP, q0 = tq * Tile::kQ;
     Tile t;
-    t.start(lds, x.ld, x.ld - p0, ld, width - q0, kStepK);
-    const uint8_t *p = reinterpret_cast<const uint8_t *>(x.x + p0);
-    const uint8_t *q = reinterpret_cast<const uint8_t *>(dz + q0);
-    t.run((*x.count + kStepK - 1) / kStepK, p, kStepK * 2 * x.ld, q, kStepK * 2 * ld);
+    t.start(lds, b.x.ld, b.x.ld - p0, b.ld, b.width - q0, kStepK);
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(b.x.x + p0);
+    const uint8_t *q = reinterpret_cast<const uint8_t *>(b.dz + q0);
+    t.run((*b.x.count + kStepK - 1) / kStepK, p, kStepK * 2 * b.x.ld, q, kStepK * 2 * b.ld);
 #pragma unroll
     for (int j = 0; j < Tile::NQ; ++j)
 #pragma unroll
         for (int i = 0; i < Tile::NP; ++i)
             t.put(lds, i, j, (gv2u){pack_bf16(t.acc[i][j][0], t.acc[i][j][1]),
                                     pack_bf16(t.acc[i][j][2], t.acc[i][j][3])});
-    t.template flush<true>(lds, dw + (int64_t)(piece0 + q0) * ld_dw + p0, ld_dw, have - q0,
-                           w.hidden - p0);
+    t.template flush<true>(lds, b.dw + (int64_t)(b.first(piece) + q0) * b.ld_dw + p0, b.ld_dw,
+                           have - q0, b.w.hidden - p0);
+}
+
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dlogits(Backward b, int piece)
+{
+    __shared__ __align__(16) uint8_t lds[Tile::kLds];
+    dlogits<Tile>(lds, b, piece, blockIdx.x);
+}
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dx(Backward b, int piece)
+{
+    __shared__ __align__(16) uint8_t lds[Tile::kLds];
+    dx_part<Tile>(lds, b, piece, blockIdx.x);
+}
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, Tile::kLds <= 32768 ? 4 : 1) void k_ce_dw(Backward b, int piece)
+{
+    __shared__ __align__(16) uint8_t lds[Tile::kLds];
+    dw_part<Tile>(lds, b, piece, blockIdx.x);
+}
+
+// dx from the slabs of sums, every row of it: 1024 columns a workgroup; p, q: the tile of
+// the products for dx
+__global__ __launch_bounds__(256) void k_ce_dx_rows(Backward b, int p, int q, bf16_t *dx, int64_t ld)
+{
+    const int hidden = b.w.hidden, wide = (hidden + 1023) / 1024;
+    const int64_t r = blockIdx.x / wide;
+    const int c = (int)(blockIdx.x % wide) * 1024 + threadIdx.x * 4;
+    if (c >= hidden)
+        return;
+    const int at = b.x.place[r];
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+    if (at >= 0) {
+        const int count = *b.x.count;
+        const int slabs = slabs_of((hidden + p - 1) / p * ((count + q - 1) / q), b.fill, b.room);
+        const float *from = b.sums + (int64_t)at * hidden + c;
+        const int64_t slab = (int64_t)count * hidden;
+#pragma unroll 8
+        for (int s = 0; s < slabs; ++s)
+            v += *reinterpret_cast<const v4f *>(from + s * slab);
+    }
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    store_vec(dx + r * ld + c, f);
 }
 
 // ---- the host's side -------------------------------------------------------------
@@ -463,6 +503,11 @@ template <class T> struct Tag {
     using Tile = T;
 };
 constexpr int kCus = 256;
+// Logits of a piece of the vocabulary: 256 MiB of dz.  (8192 x 4096 x 128256 with 2^25 to 2^28
+// of them 19.4, 18.8, 18.5 and 18.3 ms: fewer pieces add to the sums of dx less often.  Pieces
+// whose weight stays in the last-level cache leave CUs idle with few rows: 100 x 4096 x 128256
+// in pieces of 16384 1123 us, in one 737.)
+constexpr int64_t kPieceLogits = int64_t(1) << 27;
 
 // f(Tag<Tile>) for the logits of a stretch of the vocabulary.  ONCE: its weight is read by
 // nobody else soon; where all rows are one tile, it then leaves the caches to what is (24 x
@@ -524,43 +569,43 @@ ForwardPlan forward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
 }
 
 struct BackwardPlan {
-    CePacked x;
-    u16 *dz;
-    float *sums;
-    int64_t width, ld, pieces, slab, slabs, steps;
+    Backward b;  // without the caller's pointers
+    int64_t pieces;
+    int64_t dx_groups, dx_p, dx_q;  // workgroups of the products for dx, and their tile
     size_t bytes;
 };
 // a piece's width is a multiple of it, and so is how many rows dz has: of every tile's
 constexpr int kWidthStep = 256, kRowStep = 256;
 BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
 {
-    BackwardPlan b;
+    BackwardPlan f;
     Carve c = {static_cast<uint8_t *>(ws)};
+    Backward &b = f.b;
     b.x = take_packed(c, rows, hidden);
     const int64_t padded = up(rows > 0 ? rows : 1, kRowStep);
-    // Pieces of up to 64 Mi logits: 128 MiB of dz.  (Pieces whose weight stays in the
-    // last-level cache leave CUs idle with few rows: 100 x 4096 x 128256 in pieces of 16384
-    // 1123 us, in one 737.)
     const int64_t most = up(vocab, kWidthStep);
-    int64_t width = (int64_t(1) << 26) / padded / kWidthStep * kWidthStep;
+    int64_t width = kPieceLogits / padded / kWidthStep * kWidthStep;
     width = width < kWidthStep ? kWidthStep : width < most ? width : most;
-    b.width = up(tiles_of(vocab, tiles_of(vocab, width)), kWidthStep);
-    b.pieces = tiles_of(vocab, b.width);
-    b.ld = pitch(b.width);
+    width = up(tiles_of(vocab, tiles_of(vocab, width)), kWidthStep);
+    f.pieces = tiles_of(vocab, width);
+    b.width = (int)width;
+    b.ld = (int)pitch(width);
     b.dz = c.take<u16>(padded * b.ld);
-    // the vocabulary in stretches until the products for dx fill the chip
-    const int64_t room = b.width / 512 > 0 ? b.width / 512 : 1;
     with_dx(rows, [&](auto t) {
         using Tile = typename decltype(t)::Tile;
-        const int64_t tiles = tiles_of(hidden, Tile::kP) * tiles_of(rows > 0 ? rows : 1, Tile::kQ);
-        const int64_t groups = kCus * (Tile::kLds <= 65536 ? 2 : 1) * (rows <= 32 ? 2 : 1);
-        b.slabs = tiles >= groups ? 1 : groups / tiles < room ? groups / tiles : room;
+        const int64_t np = tiles_of(hidden, Tile::kP), tiles = np * tiles_of(rows, Tile::kQ);
+        b.fill = kCus * (Tile::kLds <= 65536 ? 2 : 1) * (rows <= 32 ? 2 : 1);
+        b.room = (int)(width / 512 > 0 ? width / 512 : 1);
+        // slabs x tiles are at most `fill` where there is more than one slab
+        const int64_t slab_rows = Tile::kQ * (b.fill / np);
+        const int64_t all = slab_rows < b.room * rows ? slab_rows : b.room * rows;
+        b.sums = c.take<float>((rows > all ? rows : all) * hidden);
+        f.dx_groups = tiles > b.fill ? tiles : b.fill;
+        f.dx_p = Tile::kP;
+        f.dx_q = Tile::kQ;
     });
-    b.steps = tiles_of(b.width / kStepK, b.slabs);
-    b.slab = rows * hidden;
-    b.sums = c.take<float>(b.slab * b.slabs);
-    b.bytes = c.used;
-    return b;
+    f.bytes = c.used;
+    return f;
 }
 
 bool sizes_ok(int64_t rows, int64_t hidden, int64_t vocab)
@@ -679,54 +724,53 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
         return MXQ_ERR_ALIGN;
     if (!dw && rows == 0)
         return MXQ_OK;
-    const BackwardPlan b = backward_plan(rows, hidden, vocab, workspace);
-    if (!workspace || ws_bytes < b.bytes)
+    const BackwardPlan f = backward_plan(rows, hidden, vocab, workspace);
+    if (!workspace || ws_bytes < f.bytes)
         return MXQ_ERR_WORKSPACE;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    const CeRows a = {targets, weight, rows};
-    const CeWeight cw = {static_cast<const u16 *>(w), ld_w, (int)vocab, (int)hidden};
-    const Heat heat = heat_of(temperature);
-    if (tiles_of(b.width, 128) * tiles_of(rows, 32) > INT32_MAX ||
-        tiles_of(hidden, 128) * tiles_of(rows, 32) > INT32_MAX ||
-        tiles_of(hidden, 128) * tiles_of(b.width, 128) > INT32_MAX ||
+    Backward b = f.b;
+    if (tiles_of(b.width, 128) * tiles_of(rows, 32) > INT32_MAX / 4 ||
+        tiles_of(hidden, 128) * tiles_of(rows, 32) > INT32_MAX / 4 ||
+        tiles_of(hidden, 128) * tiles_of(b.width, 128) > INT32_MAX / 4 ||
         tiles_of(hidden, 1024) * rows > INT32_MAX)
         return MXQ_ERR_SHAPE;
-    launch_pack(a, x, ld_x, hidden, b.x, true, s);
-    for (int64_t i = 0; i < b.pieces; ++i) {
-        const int piece0 = (int)(i * b.width);
-        const int64_t have = vocab - piece0 < b.width ? vocab - piece0 : b.width;
-        if (rows > 0)
-            with_logits<false>(rows, b.width, [&](auto t) {
-                using Tile = typename decltype(t)::Tile;
-                hipLaunchKernelGGL(
-                    k_ce_dlogits<Tile>,
-                    dim3((unsigned)(tiles_of(have, Tile::kP) * tiles_of(rows, Tile::kQ))),
-                    dim3(Tile::kThreads), 0, s, cw, a, b.x, heat,
-                    reinterpret_cast<const float2 *>(stats), piece0, (int)b.width, b.dz, (int)b.ld);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    b.w = {static_cast<const u16 *>(w), ld_w, (int)vocab, (int)hidden};
+    b.a = {targets, weight, rows};
+    b.heat = heat_of(temperature);
+    b.stats = reinterpret_cast<const float2 *>(stats);
+    b.dw = static_cast<u16 *>(dw);
+    b.ld_dw = ld_dw;
+    launch_pack(b.a, x, ld_x, hidden, b.x, true, s);
+    const auto have = [&](int64_t piece) {
+        return vocab - piece * b.width < b.width ? vocab - piece * b.width : (int64_t)b.width;
+    };
+    const int n_dx = dx && rows > 0 ? (int)f.dx_groups : 0;
+    with_logits<false>(rows, b.width, [&](auto tz) {
+        with_dx(rows, [&](auto tx) {
+            with_dw(rows, hidden, b.width, [&](auto tw) {
+                using Logit = typename decltype(tz)::Tile;
+                using Dx = typename decltype(tx)::Tile;
+                using Dw = typename decltype(tw)::Tile;
+                const auto n_z = [&](int64_t piece) {
+                    return tiles_of(have(piece), Logit::kP) * tiles_of(rows, Logit::kQ);
+                };
+                const auto n_dw = [&](int64_t piece) {
+                    return dw ? tiles_of(hidden, Dw::kP) * tiles_of(have(piece), Dw::kQ) : 0;
+                };
+                const auto launch = [&](auto kernel, int threads, int64_t groups, auto... args) {
+                    if (groups > 0)
+                        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), 0, s, b, args...);
+                };
+                for (int i = 0; i < (int)f.pieces; ++i) {
+                    launch(k_ce_dlogits<Logit>, Logit::kThreads, n_z(i), i);
+                    launch(k_ce_dx<Dx>, Dx::kThreads, n_dx, i);
+                    launch(k_ce_dw<Dw>, Dw::kThreads, n_dw(i), i);
+                }
             });
-        if (rows > 0 && dx)
-            with_dx(rows, [&](auto t) {
-                using Tile = typename decltype(t)::Tile;
-                hipLaunchKernelGGL(
-                    k_ce_dx<Tile>,
-                    dim3((unsigned)(tiles_of(hidden, Tile::kP) * tiles_of(rows, Tile::kQ)),
-                         (unsigned)b.slabs),
-                    dim3(Tile::kThreads), 0, s, cw, b.x, piece0, (int)b.width, (int)b.steps, b.dz,
-                    (int)b.ld, b.sums, b.slab, i > 0);
-            });
-        if (dw)
-            with_dw(rows, hidden, b.width, [&](auto t) {
-                using Tile = typename decltype(t)::Tile;
-                hipLaunchKernelGGL(
-                    k_ce_dw<Tile>,
-                    dim3((unsigned)(tiles_of(hidden, Tile::kP) * tiles_of(have, Tile::kQ))),
-                    dim3(Tile::kThreads), 0, s, cw, b.x, piece0, (int)b.width, b.dz, (int)b.ld,
-                    static_cast<u16 *>(dw), ld_dw);
-            });
-    }
-    if (dx && rows > 0)
+        });
+    });
+    if (n_dx > 0)
         hipLaunchKernelGGL(k_ce_dx_rows, dim3((unsigned)(rows * tiles_of(hidden, 1024))), dim3(256),
-                           0, s, rows, (int)hidden, b.x.place, b.sums, b.slab, (int)b.slabs,
-                           static_cast<bf16_t *>(dx), ld_dx);
+                           0, s, b, (int)f.dx_p, (int)f.dx_q, static_cast<bf16_t *>(dx), ld_dx);
     return launched();
 }
