@@ -131,21 +131,21 @@ template <bool P_ALONG, bool Q_ALONG, bool ONCE = false>
 using Twin = Product<4, 1, 2, 8, 2, P_ALONG, Q_ALONG, ONCE>;  // 128 x 128
 // Few rows, where the weight is what there is to read
 template <bool P_ALONG, bool Q_ALONG, bool ONCE = false>
-using Few = Product<4, 1, 2, 2, 4, P_ALONG, Q_ALONG, ONCE>;  // 128 x 32
+using Few = Product<4, 1, 2, 2, 3, P_ALONG, Q_ALONG, ONCE>;  // 128 x 32
 // dw of rows that are one step of the product over them
 using Outer = Product<2, 2, 4, 4, 1, false, false>;  // 128 x 128
 
-// the tile's product: w rows from p0, packed x rows from q0
-template <class Tile>
+// the tile's product: w rows from p0, packed x rows from q0; meanwhile: see Product::run
+template <class Tile, class F>
 __device__ __forceinline__ void logits(Tile &t, uint8_t *lds, const CeWeight &w,
-                                       const CePacked &x, int p0, int count, int q0)
+                                       const CePacked &x, int p0, int count, int q0, F meanwhile)
 {
     const int rows = (count + kStepK - 1) / kStepK * kStepK;
     t.start(lds, w.ld, w.vocab - p0, x.ld, rows - q0, w.hidden);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w.w + (int64_t)p0 * w.ld);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(x.x + (int64_t)q0 * x.ld);
     const int steps = (w.hidden + kStepK - 1) / kStepK;
-    t.run(steps, p, kStepK * 2, q, kStepK * 2, (int)(blockIdx.x & 7) * steps / 8);
+    t.run(steps, p, kStepK * 2, q, kStepK * 2, (int)(blockIdx.x & 7) * steps / 8, meanwhile);
 }
 
 // Maximum and sum of every packed row over the tile's vocabulary, and the logit at its
@@ -163,15 +163,19 @@ __global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_stats(CeWeight w, CeRo
     int tp, tq;
     product_tile(blockIdx.x, np, nq, tp, tq);
     const int p0 = tp * Tile::kP, q0 = tq * Tile::kQ;
+    __shared__ int targets[Tile::kQ];  // of the tile's rows, within the tile
     Tile t;
-    logits(t, lds, w, x, p0, count, q0);
+    logits(t, lds, w, x, p0, count, q0, [&] {
+        for (int q = threadIdx.x; q < Tile::kQ; q += Tile::kThreads)
+            targets[q] = q0 + q < count ? a.targets[x.row[q0 + q]] - p0 : -1;
+    });
 
     float2 *joint = reinterpret_cast<float2 *>(lds);  // [WP][kQ]
     const bool whole = p0 + Tile::kP <= w.vocab;
 #pragma unroll
     for (int j = 0; j < Tile::NQ; ++j) {
         const int q = t.q_of(j);
-        const int target = q0 + q < count ? a.targets[x.row[q0 + q]] - p0 : -1;
+        const int target = targets[q];
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < Tile::NP; ++i)
@@ -309,22 +313,34 @@ template <class Tile> __device__ __forceinline__ void dlogits(uint8_t *lds, cons
     int tp, tq;
     product_tile(at, np, nq, tp, tq);
     const int p0 = b.first(piece) + tp * Tile::kP, q0 = tq * Tile::kQ;
+    // what the tile's rows take: the maximum, weight / (T s), weight / T and the target within
+    // the tile
+    __shared__ float4 rows_of[Tile::kQ];
     Tile t;
-    logits(t, lds, b.w, b.x, p0, count, q0);
+    logits(t, lds, b.w, b.x, p0, count, q0, [&] {
+        for (int q = threadIdx.x; q < Tile::kQ; q += Tile::kThreads) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
+            if (q0 + q < count) {
+                const int row = b.x.row[q0 + q];
+                const int target = b.a.targets[row];
+                const float2 st = b.stats[row];
+                float scale = (b.a.weight ? b.a.weight[row] : 1.0f) * b.heat.inv;
+                if (target >= b.w.vocab)
+                    scale = NAN;
+                v = make_float4(base_of(st.x), st.y == 0.0f ? 0.0f : scale / st.y, scale,
+                                __int_as_float(target - p0));
+            }
+            rows_of[q] = v;
+        }
+    });
     const bool whole = p0 + Tile::kP <= b.w.vocab;
 #pragma unroll
     for (int j = 0; j < Tile::NQ; ++j) {
-        const int q = q0 + t.q_of(j);
-        const bool in = q < count;
-        const int row = in ? b.x.row[q] : 0;
-        const int target = in ? b.a.targets[row] : -1;
-        const float2 st = in ? b.stats[row] : make_float2(0.0f, 1.0f);
-        float scale = in ? (b.a.weight ? b.a.weight[row] : 1.0f) * b.heat.inv : 0.0f;
-        if (target >= b.w.vocab)
-            scale = NAN;
-        const float base = base_of(st.x);
-        const float inv = st.y == 0.0f ? 0.0f : scale / st.y;
-        const bool near = __any((unsigned)(target - p0) < (unsigned)Tile::kP);
+        const bool in = q0 + t.q_of(j) < count;
+        const float4 row = rows_of[t.q_of(j)];
+        const float base = row.x, inv = row.y, scale = row.z;
+        const int target = __float_as_int(row.w);
+        const bool near = __any((unsigned)target < (unsigned)Tile::kP);
 #pragma unroll
         for (int i = 0; i < Tile::NP; ++i) {
             float d[4];
@@ -334,7 +350,7 @@ template <class Tile> __device__ __forceinline__ void dlogits(uint8_t *lds, cons
             if (near) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    d[r] -= p0 + t.p_of(i) + r == target ? scale : 0.0f;
+                    d[r] -= t.p_of(i) + r == target ? scale : 0.0f;
             }
             if (!whole || q0 + Tile::kQ > count) {
 #pragma unroll
@@ -379,7 +395,7 @@ template <class Tile> __device__ __forceinline__ void dx_part(uint8_t *lds, cons
     const uint8_t *q = reinterpret_cast<const uint8_t *>(b.dz + (int64_t)q0 * b.ld + v0);
     // dz is zero behind the vocabulary's last
     t.start(lds, b.w.ld, b.w.hidden - p0, b.ld, Tile::kQ, max(0, have));
-    t.run(n, p, kStepK * 2 * (uint32_t)b.w.ld, q, kStepK * 2);
+    t.run(n, p, kStepK * 2 * (uint32_t)b.w.ld, q, kStepK * 2, 0, [] {});
     float *to = b.sums + (int64_t)slab * count * b.w.hidden;
 #pragma unroll
     for (int j = 0; j < Tile::NQ; ++j)
@@ -408,7 +424,8 @@ template <class Tile> __device__ __forceinline__ void dw_part(uint8_t *lds, cons
     t.start(lds, b.x.ld, b.x.ld - p0, b.ld, b.width - q0, kStepK);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(b.x.x + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(b.dz + q0);
-    t.run((*b.x.count + kStepK - 1) / kStepK, p, kStepK * 2 * b.x.ld, q, kStepK * 2 * b.ld);
+    t.run((*b.x.count + kStepK - 1) / kStepK, p, kStepK * 2 * b.x.ld, q, kStepK * 2 * b.ld, 0,
+          [] {});
 #pragma unroll
     for (int j = 0; j < Tile::NQ; ++j)
 #pragma unroll

@@ -245,9 +245,11 @@ struct Product {
     // read when its first half is done: there, once a step, is the barrier, and the step
     // SLOTS further is fetched behind it into the same slot.  With two slots it lands during
     // the second half and the next step's first one.
-    // The steps are taken in a circle from step `first`.
+    // The steps are taken in a circle from step `first`.  meanwhile() runs while the first
+    // steps are fetched; the workgroup meets a barrier behind it.
+    template <class F>
     __device__ __forceinline__ void run(int steps, const uint8_t *p, uint32_t dp, const uint8_t *q,
-                                        uint32_t dq, int first = 0)
+                                        uint32_t dq, int first, F meanwhile)
     {
         if (steps <= 0)
             return;
@@ -266,6 +268,7 @@ struct Product {
             }
         // of `left` steps that are fetched, the first has landed
         const auto landed = [&](int left) { wait_behind<SLOTS>(left); };
+        meanwhile();
         landed(min(steps, SLOTS));
         barrier_no_fence();
         v8bf fp[2][NP], fq[2][NQ];
