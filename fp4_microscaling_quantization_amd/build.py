@@ -7,7 +7,7 @@ instructions disabled.
 
 Beside it stands libmxq_loop.so, for the tests: the same library with launches
 over rows of at most LOOP_GRID workgroups, so that few rows make every
-workgroup take several in turn.
+workgroup take several in turn, and with pieces of the vocabulary of one tile.
 """
 import glob
 import os
@@ -18,7 +18,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmxq.so")
 LOOP_LIB = os.path.join(HERE, "libmxq_loop.so")
 LOOP_GRID = 5
-LOOP_SOURCES = ("norm.hip", "logprobs.hip", "distill.hip")
+LOOP_SOURCES = ("norm.hip", "logprobs.hip", "distill.hip", "linear_ce.hip")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
@@ -59,7 +59,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
         name = os.path.basename(src)
         objs.append(compile_to(src, os.path.join(objdir, name + ".o"), []))
         loop_objs.append(compile_to(src, os.path.join(objdir, name + ".loop.o"),
-                                    [f"-DMXQ_ROW_GRID={LOOP_GRID}"]) if name in LOOP_SOURCES else objs[-1])
+                                    [f"-DMXQ_ROW_GRID={LOOP_GRID}", "-DMXQ_PIECE_LOGITS=1"]) if name in LOOP_SOURCES else objs[-1])
     for p in procs:
         _wait(p)
     link(objs, LIB)

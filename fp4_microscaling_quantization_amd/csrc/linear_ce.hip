@@ -455,34 +455,38 @@ __global__ __launch_bounds__(Tile::kThreads, Tile::kLds <= 32768 ? 4 : 1) void k
     dw_part<Tile>(lds, b, piece, blockIdx.x);
 }
 
-// dx from the slabs of sums, every row of it: 1024 columns a workgroup; p, q: the tile of
-// the products for dx
+// dx from the slabs of sums, every row of it, 1024 columns at a time; p, q: the tile of the
+// products for dx
 __global__ __launch_bounds__(256) void k_ce_dx_rows(Backward b, int p, int q, bf16_t *dx, int64_t ld)
 {
     const int hidden = b.w.hidden, wide = (hidden + 1023) / 1024;
-    const int64_t r = blockIdx.x / wide;
-    const int c = (int)(blockIdx.x % wide) * 1024 + threadIdx.x * 4;
-    if (c >= hidden)
-        return;
-    const int at = b.x.place[r];
-    v4f v = {0.f, 0.f, 0.f, 0.f};
-    if (at >= 0) {
-        const int count = *b.x.count;
-        const int slabs = slabs_of((hidden + p - 1) / p * ((count + q - 1) / q), b.fill, b.room);
-        const float *from = b.sums + (int64_t)at * hidden + c;
-        const int64_t slab = (int64_t)count * hidden;
+    const int count = *b.x.count;
+    const int slabs = slabs_of((hidden + p - 1) / p * ((count + q - 1) / q), b.fill, b.room);
+    const int64_t slab = (int64_t)count * hidden;
+    for (int64_t i = blockIdx.x; i < b.a.rows * wide; i += gridDim.x) {
+        const int64_t r = i / wide;
+        const int c = (int)(i % wide) * 1024 + threadIdx.x * 4;
+        if (c >= hidden)
+            continue;
+        const int at = b.x.place[r];
+        v4f v = {0.f, 0.f, 0.f, 0.f};
+        if (at >= 0) {
+            const float *from = b.sums + (int64_t)at * hidden + c;
 #pragma unroll 8
-        for (int s = 0; s < slabs; ++s)
-            v += *reinterpret_cast<const v4f *>(from + s * slab);
+            for (int s = 0; s < slabs; ++s)
+                v += *reinterpret_cast<const v4f *>(from + s * slab);
+        }
+        const float f[4] = {v[0], v[1], v[2], v[3]};
+        store_vec(dx + r * ld + c, f);
     }
-    const float f[4] = {v[0], v[1], v[2], v[3]};
-    store_vec(dx + r * ld + c, f);
 }
 
 // ---- the host's side -------------------------------------------------------------
 
-constexpr int64_t kMostRows = INT32_MAX - 255;
-constexpr int64_t kMostLd = int64_t(1) << 22;  // 256 rows of it: an offset of 32 bits
+// What is taken: offsets within a tile fit 32 bits, and launches their number of threads.
+constexpr int64_t kMostRows = int64_t(1) << 22, kMostVocab = int64_t(1) << 24;
+constexpr int64_t kMostHidden = int64_t(1) << 16, kMostLogits = int64_t(1) << 37;
+constexpr int64_t kMostLd = int64_t(1) << 22;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
@@ -524,7 +528,11 @@ constexpr int kCus = 256;
 // of them 19.4, 18.8, 18.5 and 18.3 ms: fewer pieces add to the sums of dx less often.  Pieces
 // whose weight stays in the last-level cache leave CUs idle with few rows: 100 x 4096 x 128256
 // in pieces of 16384 1123 us, in one 737.)
-constexpr int64_t kPieceLogits = int64_t(1) << 27;
+// (The tests have a build whose pieces are a tile wide.)
+#ifndef MXQ_PIECE_LOGITS
+#define MXQ_PIECE_LOGITS (1 << 27)
+#endif
+constexpr int64_t kPieceLogits = MXQ_PIECE_LOGITS;
 
 // f(Tag<Tile>) for the logits of a stretch of the vocabulary.  ONCE: its weight is read by
 // nobody else soon; where all rows are one tile, it then leaves the caches to what is (24 x
@@ -627,8 +635,8 @@ BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws
 
 bool sizes_ok(int64_t rows, int64_t hidden, int64_t vocab)
 {
-    return rows >= 0 && rows <= kMostRows && vocab >= 1 && vocab <= kMaxVocab - 256 &&
-           hidden >= 32 && hidden % 32 == 0 && hidden <= kMostLd;
+    return rows >= 0 && rows <= kMostRows && vocab >= 1 && vocab <= kMostVocab &&
+           rows * vocab <= kMostLogits && hidden >= 32 && hidden % 32 == 0 && hidden <= kMostHidden;
 }
 
 mxq_status check(const void *x, int64_t ld_x, const void *w, int64_t ld_w, int64_t rows,
@@ -700,8 +708,6 @@ extern "C" mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const v
     return with_logits<true>(rows, vocab, [&](auto t) {
         using Tile = typename decltype(t)::Tile;
         const int64_t groups = f.tiles * tiles_of(rows, Tile::kQ);
-        if (groups > INT32_MAX)
-            return (mxq_status)MXQ_ERR_SHAPE;
         launch_pack(a, x, ld_x, hidden, f.x, false, s);
         hipLaunchKernelGGL(k_ce_stats<Tile>, dim3((unsigned)groups), dim3(Tile::kThreads), 0, s, cw,
                            a, f.x, heat, f.part, f.stride);
@@ -745,11 +751,6 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
     if (!workspace || ws_bytes < f.bytes)
         return MXQ_ERR_WORKSPACE;
     Backward b = f.b;
-    if (tiles_of(b.width, 128) * tiles_of(rows, 32) > INT32_MAX / 4 ||
-        tiles_of(hidden, 128) * tiles_of(rows, 32) > INT32_MAX / 4 ||
-        tiles_of(hidden, 128) * tiles_of(b.width, 128) > INT32_MAX / 4 ||
-        tiles_of(hidden, 1024) * rows > INT32_MAX)
-        return MXQ_ERR_SHAPE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     b.w = {static_cast<const u16 *>(w), ld_w, (int)vocab, (int)hidden};
     b.a = {targets, weight, rows};
@@ -787,7 +788,7 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
         });
     });
     if (n_dx > 0)
-        hipLaunchKernelGGL(k_ce_dx_rows, dim3((unsigned)(rows * tiles_of(hidden, 1024))), dim3(256),
+        hipLaunchKernelGGL(k_ce_dx_rows, dim3(row_grid(rows * tiles_of(hidden, 1024))), dim3(256),
                            0, s, b, (int)f.dx_p, (int)f.dx_q, static_cast<bf16_t *>(dx), ld_dx);
     return launched();
 }

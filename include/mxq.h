@@ -470,7 +470,7 @@ mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t ro
  *  - x [rows x hidden], w [vocab x hidden], dx, dw (as x, w) are bf16.  hidden is a
  *    multiple of 32.  w and dw are 16-byte aligned, their leading dimensions
  *    multiples of 8 and at most 2^22; x and dx stand at any element.  hidden is
- *    at most 2^22, vocab less than 2^31 - 512, rows less than 2^31 - 255.
+ *    at most 2^16, vocab 2^24, rows 2^22, rows x vocab 2^37.
  *  - Products of bf16 values are summed in fp32; dz is rounded to bf16 once,
  *    dx and dw where they are stored.
  *  - A row with a target < 0 or a weight of 0 does not count: loss 0, stats

@@ -16,9 +16,10 @@ NAN, INF = float("nan"), float("inf")
 def ce_refusals(m, f):
     for t in (0.0, -1.0, NAN, INF, 1e-40):
         assert f(t=t) == m.ERR_UNSUPPORTED
-    assert f(rows=-1) == f(rows=(1 << 31) - 255) == f(vocab=0) == f(vocab=-5) == f(vocab=1 << 31) == m.ERR_SHAPE
+    assert f(rows=-1) == f(rows=(1 << 22) + 1) == f(vocab=0) == f(vocab=-5) == f(vocab=(1 << 24) + 1) == m.ERR_SHAPE
+    assert f(rows=1 << 20, vocab=(1 << 17) + 1) == f(rows=1 << 62, vocab=1 << 62) == m.ERR_SHAPE
     assert f(hidden=0) == f(hidden=48) == f(hidden=-32) == f(ldx=95) == f(ldw=95) == m.ERR_SHAPE
-    assert f(hidden=1 << 23, ldx=1 << 23, ldw=1 << 23) == f(ldw=(1 << 22) + 8) == m.ERR_SHAPE
+    assert f(hidden=(1 << 16) + 32, ldx=1 << 20, ldw=1 << 20, lddx=1 << 20, lddw=1 << 20) == f(ldw=(1 << 22) + 8) == m.ERR_SHAPE
     assert f(x=None) == f(w=None) == f(targets=None) == m.ERR_NULL
     assert f(x=A + 1) == f(w=B + 8) == f(ldw=100) == f(targets=D + 2) == f(weight=D + 1) == m.ERR_ALIGN
 
@@ -27,10 +28,10 @@ def test_linear_ce_forward_refusals(mxq_lib):
     m, L = mxq_lib, mxq_lib.lib()
     need = L.mxq_linear_ce_forward_workspace_size(4, 96, 100)
     assert need > 0
-    for bad in ((-1, 96, 100), (0, 96, 100), (4, 95, 100), (4, 0, 100), (4, 96, 0), (4, 96, 1 << 31), (1 << 31, 96, 100)):
+    for bad in ((-1, 96, 100), (0, 96, 100), (4, 95, 100), (4, 0, 100), (4, 96, 0), (4, 96, 1 << 31), (1 << 31, 96, 100), (1 << 20, 96, 1 << 18), (4, 1 << 17, 100)):
         assert L.mxq_linear_ce_forward_workspace_size(*bad) == 0
 
-    def f(x=A, ldx=96, w=B, ldw=96, rows=4, hidden=96, vocab=100, t=1.0, targets=D, weight=None, loss=E, stats=F, ws=A, size=need):
+    def f(x=A, ldx=96, w=B, ldw=96, rows=4, hidden=96, vocab=100, t=1.0, targets=D, weight=None, loss=E, stats=F, ws=A, size=need, **_):
         return L.mxq_linear_ce_forward(x, ldx, w, ldw, rows, hidden, vocab, t, targets, weight, loss, stats, ws, size, None)
     ce_refusals(m, f)
     assert f(loss=None) == f(stats=None) == m.ERR_NULL
