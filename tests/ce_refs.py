@@ -23,9 +23,10 @@ U, H = 2.0 ** -24, 2.0 ** -8
 
 
 class HeadLoss:
-    """loss, stats, dx, dw of the rows x [rows, hidden] under w [vocab, hidden], on the CPU."""
+    """loss, stats, dx, dw of the rows x [rows, hidden] under w [vocab, hidden], on the CPU; the gradients
+    from `stats` where they are given."""
 
-    def __init__(self, x, w, targets, weight=None, t=1.0):
+    def __init__(self, x, w, targets, weight=None, t=1.0, stats=None):
         x, w = x.double().cpu(), w.double().cpu()
         targets = targets.long().cpu()
         rows, hidden = x.shape
@@ -58,6 +59,10 @@ class HeadLoss:
         self.s, self.d_s = torch.ones(rows, dtype=torch.float64), torch.zeros(rows, dtype=torch.float64)
         self.m[k], self.d_m[k] = m[:, 0], d_z.amax(1)
         self.s[k], self.d_s[k] = s[:, 0], d_s[:, 0]
+        if stats is not None:
+            given = stats.double().cpu()[k]
+            a, s = (z - given[:, :1]) / t, given[:, 1:]
+            e, d_a, d_s = a.exp(), d_z / t, 0 * s
         q = e / s
         one = torch.zeros_like(q).scatter_(1, at, 1.0)
         dz = w1 / t * (q - one)

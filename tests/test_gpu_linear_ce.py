@@ -60,7 +60,7 @@ def test_placement(mxq_lib, shape):
     x, w, targets, weight = case(*shape, seed=11, ignored=0.2)
     want = HeadLoss(x, w, targets, weight, 1.0)
     td, gd, sd = targets.to(dev()), weight.to(dev()), want.stats().to(dev())
-    for pad, shift, pad_w, shift_w in ((0, 1, 0, 8), (3, 0, 8, 0), (5, 7, 40, 16)):
+    for pad, shift, pad_w, shift_w in ((0, 1, 0, 8), (3, 0, 8, 0), (5, 7, 40, 16), (8, 8, 0, 0), (64, 0, 8, 8)):
         say("placement", shape, pad, shift)
         xd, _ = placed(x, pad, shift)
         wd, _ = placed(w, pad_w, shift_w)
