@@ -191,6 +191,33 @@ def test_gradient_against_differences(mxq_lib):
             assert abs(got - slope) <= 2.0 ** -6 * (got.abs() + rms * u.abs().sum()), (got, slope)
 
 
+@pytest.mark.parametrize("weight,t", [(1 + 2.0 ** -8, 1.0), (1 / 1351, 0.7), (-3.0, 2.0)])
+def test_rounding_is_not_the_same_for_all(mxq_lib, weight, t):
+    """With all weights alike, dx and dw are not off by one factor.  Their best factor against the formulas
+    is an average of the roundings: of dz over 600 rows, each at most 2^-8 / sqrt(3) of itself in the root
+    mean square, and of the many more stored values; seven deviations of both are below 2^-8 / 3.  (Halfway
+    between two bf16 numbers, 1 + 2^-8 alone would put them all off by 2^-8.)"""
+    x, w, targets, _ = case(600, 128, 1031, 43)
+    weight = torch.full((600,), weight)
+    want = HeadLoss(x, w, targets, weight, t)
+    _, _, dx, dw = run_both(mxq_lib, x, w, targets, weight, t, want)
+    for got, exact in ((dx, want.dx), (dw, want.dw)):
+        factor = (got.double().cpu() * exact).sum() / exact.square().sum()
+        assert abs(factor - 1) <= 2.0 ** -8 / 3, factor
+
+
+def test_weights_that_are_no_numbers(mxq_lib):
+    """The first row's weight says nothing about the others': it may be NaN, infinite, subnormal or huge."""
+    d = dev()
+    x, w, targets, weight = case(70, 64, 300, 47)
+    want = HeadLoss(x, w, targets, weight, 1.0)
+    import row_refs as ref
+    for first in (NAN, INF, 1e-42, 3e38, -1e-30):
+        weight[0] = first
+        dx, _ = mxq_lib.linear_ce_backward(x.to(d), w.to(d), targets.to(d), want.stats().to(d), weight.to(d))
+        ref.check(("dx", first), dx[1:], want.dx[1:], want.d_dx[1:])
+
+
 def test_repeats_and_graph(mxq_lib):
     """The same bits each time, and from a replayed graph, between eager calls on other data."""
     d = dev()
