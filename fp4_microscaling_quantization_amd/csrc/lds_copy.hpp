@@ -74,6 +74,20 @@ __device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32
                      : "memory");
 }
 
+// The same from an address of each lane's own.
+__device__ __forceinline__ void copy16(const uint8_t *from, uint32_t lds)
+{
+    uint32_t saved;
+    asm volatile("s_mov_b32 %0, m0\n\t"
+                 "s_mov_b32 m0, %2\n\t"
+                 "s_nop 0\n\t"
+                 "global_load_lds_dwordx4 %1, off\n\t"
+                 "s_mov_b32 m0, %0"
+                 : "=&s"(saved)
+                 : "v"(from), "s"(lds)
+                 : "memory");
+}
+
 __device__ __forceinline__ void wait_all_vm()
 {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), expcnt/lgkmcnt untouched

@@ -139,20 +139,23 @@ __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per,
 
 // ---- logits ----------------------------------------------------------------------
 
-// Tiles, p x q.  Many: for products that fill the chip with them.
-template <bool P_ALONG, bool Q_ALONG> using Many = Product<2, 4, 8, 4, 2, P_ALONG, Q_ALONG>;  // 256 x 256
+// Tiles, p x q.  Many: for products that fill the chip with them.  CUT, ONCE: P_CUT, P_ONCE.
+template <bool P_ALONG, bool Q_ALONG, bool CUT>
+using Many = Product<2, 4, 8, 4, 2, P_ALONG, Q_ALONG, CUT>;  // 256 x 256
 // For those that do not: half as large, and a step more in flight.
-template <bool P_ALONG, bool Q_ALONG> using Half = Product<2, 4, 4, 4, 3, P_ALONG, Q_ALONG>;  // 128 x 256
+template <bool P_ALONG, bool Q_ALONG, bool CUT>
+using Half = Product<2, 4, 4, 4, 3, P_ALONG, Q_ALONG, CUT>;  // 128 x 256
 // A quarter: one to a CU with four steps in LDS, two with two.
-template <bool P_ALONG, bool Q_ALONG, bool ONCE = false>
-using Deep = Product<4, 2, 2, 4, 4, P_ALONG, Q_ALONG, ONCE>;  // 128 x 128
-template <bool P_ALONG, bool Q_ALONG, bool ONCE = false>
-using Twin = Product<4, 1, 2, 8, 2, P_ALONG, Q_ALONG, ONCE>;  // 128 x 128
-// Few rows, where the weight is what there is to read
-template <bool P_ALONG, bool Q_ALONG, bool ONCE = false>
-using Few = Product<4, 1, 2, 2, 3, P_ALONG, Q_ALONG, ONCE>;  // 128 x 32
+template <bool P_ALONG, bool Q_ALONG, bool CUT, bool ONCE = false>
+using Deep = Product<4, 2, 2, 4, 4, P_ALONG, Q_ALONG, CUT, ONCE>;  // 128 x 128
+template <bool P_ALONG, bool Q_ALONG, bool CUT, bool ONCE = false>
+using Twin = Product<4, 1, 2, 8, 2, P_ALONG, Q_ALONG, CUT, ONCE>;  // 128 x 128
+// Few rows, where the weight is what there is to read.  (16 rows under 32003 x 4096 56 us with
+// three or four steps in LDS, 69 with two.)
+template <bool P_ALONG, bool Q_ALONG, bool CUT, bool ONCE = false>
+using Few = Product<4, 1, 2, 2, 3, P_ALONG, Q_ALONG, CUT, ONCE>;  // 128 x 32
 // dw of rows that are one step of the product over them
-using Outer = Product<2, 2, 4, 4, 1, false, false>;  // 128 x 128
+using Outer = Product<2, 2, 4, 4, 1, false, false, false>;  // 128 x 128
 
 // the tile's product: w rows from p0, packed x rows from q0; meanwhile: see Product::run
 template <class Tile, class F>
@@ -563,40 +566,52 @@ constexpr int64_t kPieceLogits = MXQ_PIECE_LOGITS;
 // f(Tag<Tile>) for the logits of a stretch of the vocabulary.  ONCE: its weight is read by
 // nobody else soon; where all rows are one tile, it then leaves the caches to what is (24 x
 // 4096 x 128256 in the forward pass 205 us without the hint, 182 with it).
-template <bool ONCE, class F> auto with_logits(int64_t rows, int64_t vocab, F f)
+template <bool ONCE, bool CUT, class F> void with_logits_of(int64_t rows, int64_t vocab, F f)
 {
-    if (rows <= 32)
-        return f(Tag<Few<true, true, ONCE>>{});
-    // 100 rows under 32000 x 4096 (250 tiles) Deep 64 us, Twin 78; under 128256 x 4096 222 and 203
-    if (rows <= 128) {
-        if (tiles_of(vocab, 128) <= kCus)
-            return f(Tag<Deep<true, true, ONCE>>{});
-        return f(Tag<Twin<true, true, ONCE>>{});
-    }
+    // 100 rows under 32000 x 4096 (250 tiles) Deep 64 us, Twin 78; under 128256 x 4096 222 and 203;
     // 200 rows under 32000 x 4096 (125 tiles) Half 79 us, Many 126; 400 rows (250) 153 and 135
-    if (tiles_of(vocab, 256) * tiles_of(rows, 256) <= kCus / 2)
-        return f(Tag<Half<true, true>>{});
-    return f(Tag<Many<true, true>>{});
+    if (rows <= 32)
+        f(Tag<Few<true, true, CUT, ONCE>>{});
+    else if (rows <= 128 && tiles_of(vocab, 128) <= kCus)
+        f(Tag<Deep<true, true, CUT, ONCE>>{});
+    else if (rows <= 128)
+        f(Tag<Twin<true, true, CUT, ONCE>>{});
+    else if (tiles_of(vocab, 256) * tiles_of(rows, 256) <= kCus / 2)
+        f(Tag<Half<true, true, CUT>>{});
+    else
+        f(Tag<Many<true, true, CUT>>{});
+}
+template <bool ONCE, class F>
+void with_logits(int64_t rows, int64_t hidden, int64_t vocab, F f)
+{
+    // looking for a last step that is not whole, along k, costs 2 to 4%
+    if (hidden % kStepK)
+        with_logits_of<ONCE, true>(rows, vocab, f);
+    else
+        with_logits_of<ONCE, false>(rows, vocab, f);
 }
 // for dx, whose tiles are made enough by stretches of the vocabulary
-template <class F> auto with_dx(int64_t rows, F f)
+template <class F> void with_dx(int64_t rows, F f)
 {
     if (rows <= 32)
-        return f(Tag<Few<false, true>>{});
-    if (rows <= 128)
-        return f(Tag<Twin<false, true>>{});
-    return f(Tag<Many<false, true>>{});
+        f(Tag<Few<false, true, true>>{});
+    else if (rows <= 128)
+        f(Tag<Twin<false, true, true>>{});
+    else
+        f(Tag<Many<false, true, true>>{});
 }
 // for dw
-template <class F> auto with_dw(int64_t rows, int64_t hidden, int64_t vocab, F f)
+template <class F> void with_dw(int64_t rows, int64_t hidden, int64_t vocab, F f)
 {
+    // 1024 rows under 8000 x 512 (64 tiles) forward and backward Deep 70 us, Many 83
     if (rows <= kStepK)
-        return f(Tag<Outer>{});
-    if (tiles_of(vocab, 256) * tiles_of(hidden, 256) <= kCus / 2)
-        return f(Tag<Deep<false, false>>{});
-    if (rows <= 2 * kStepK)
-        return f(Tag<Twin<false, false>>{});
-    return f(Tag<Many<false, false>>{});
+        f(Tag<Outer>{});
+    else if (tiles_of(vocab, 256) * tiles_of(hidden, 256) <= kCus / 2)
+        f(Tag<Deep<false, false, false>>{});
+    else if (rows <= 2 * kStepK)
+        f(Tag<Twin<false, false, false>>{});
+    else
+        f(Tag<Many<false, false, false>>{});
 }
 
 struct ForwardPlan {
@@ -610,7 +625,7 @@ ForwardPlan forward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
     ForwardPlan f;
     Carve c = {static_cast<uint8_t *>(ws)};
     f.x = take_packed(c, rows, hidden);
-    with_logits<true>(rows, vocab, [&](auto t) {
+    with_logits<true>(rows, hidden, vocab, [&](auto t) {
         f.tiles = tiles_of(vocab, decltype(t)::Tile::kP);
     });
     f.stride = up(rows, 16);
@@ -731,7 +746,7 @@ extern "C" mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const v
     const CeRows a = {targets, weight, rows};
     const CeWeight cw = {static_cast<const u16 *>(w), ld_w, (int)vocab, (int)hidden};
     const Heat heat = heat_of(temperature);
-    return with_logits<true>(rows, vocab, [&](auto t) {
+    with_logits<true>(rows, hidden, vocab, [&](auto t) {
         using Tile = typename decltype(t)::Tile;
         const int64_t groups = f.tiles * tiles_of(rows, Tile::kQ);
         // Rows that are all of one tile are read where they are, if they can be: the ones that do
@@ -758,8 +773,8 @@ extern "C" mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const v
             loss_of(std::integral_constant<int, 1>{});
         else
             loss_of(std::integral_constant<int, 16>{});
-        return launched();
     });
+    return launched();
 }
 
 extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const void *w,
@@ -799,7 +814,7 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
         return vocab - piece * b.width < b.width ? vocab - piece * b.width : (int64_t)b.width;
     };
     const int n_dx = dx && rows > 0 ? (int)f.dx_groups : 0;
-    with_logits<false>(rows, b.width, [&](auto tz) {
+    with_logits<false>(rows, hidden, b.width, [&](auto tz) {
         with_dx(rows, [&](auto tx) {
             with_dw(rows, hidden, b.width, [&](auto tw) {
                 using Logit = typename decltype(tz)::Tile;

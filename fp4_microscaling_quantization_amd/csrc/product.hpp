@@ -32,6 +32,8 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
+__device__ const __attribute__((aligned(16))) uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
+
 constexpr int kStepK = 64;  // k of a step: two halves of one fragment's 32 each
 
 // One operand's tile of ROWS rows.
@@ -41,15 +43,19 @@ template <int ROWS, bool ALONG> struct Side {
     static_assert(ALONG || ROWS >= 128, "fragments across k are read from 256 bytes and more");
 
     // What lane `lane` fetches for copy cc of a step, in bytes from the tile's first
-    // element; ld in elements; rows past the last of `have` >= 1 and k past the last of
-    // `have_k` fetch an earlier one (their products are not used, or are with zeros).
+    // element; ld in elements; rows past the last of `have` >= 1 fetch it again (their
+    // products are not used).  k past the last of `have_k`: kNone along k, else the last one
+    // again (their products are with zeros).
+    static constexpr uint32_t kNone = ~0u;
     static __device__ __forceinline__ uint32_t offset(int cc, int lane, int64_t ld, int have,
                                                       int have_k = kStepK)
     {
         if constexpr (ALONG) {
             const int row = 8 * cc + (lane >> 3);
             const int chunk = (lane & 7) ^ ((row >> 1) & 7);
-            return (uint32_t)(min(row, have - 1) * ld * 2 + min(chunk * 8, have_k - 8) * 2);
+            if (chunk * 8 >= have_k)
+                return kNone;
+            return (uint32_t)(min(row, have - 1) * ld * 2 + chunk * 16);
         } else {
             constexpr int PER = ROWS / 8;  // chunks of one k
             const int k = cc * (64 / PER) + lane / PER;
@@ -123,8 +129,9 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
 }
 
 // A workgroup of WP x WQ waves, each with NP x NQ tiles of 16 x 16, and SLOTS steps in LDS
-// (1: there is one step only).  P_ONCE: P is not read again.
-template <int WP_, int WQ_, int NP_, int NQ_, int SLOTS, bool P_ALONG, bool Q_ALONG,
+// (1: there is one step only).  P_CUT: the last step of P may have fewer k, where Q is zero.
+// P_ONCE: P is not read again.
+template <int WP_, int WQ_, int NP_, int NQ_, int SLOTS, bool P_ALONG, bool Q_ALONG, bool P_CUT,
           bool P_ONCE = false>
 struct Product {
     static constexpr int WP = WP_, WQ = WQ_, NP = NP_, NQ = NQ_;
@@ -161,7 +168,7 @@ struct Product {
     typename SideQ::template Reader<WQ> read_q;
     uint32_t off_p[kPerP], off_q[kPerQ];
     uint32_t at_p, at_q;  // the wave's first copies in LDS
-    // a last step with fewer k, and what is fetched of P there (Q is zero behind it)
+    // P_CUT: a last step with fewer k, and what is fetched of P there (Q is zero behind it)
     int cut_step;
     uint32_t cut_p[kPerP];
 
@@ -188,7 +195,8 @@ struct Product {
 #pragma unroll
         for (int i = 0; i < kPerP; ++i) {
             off_p[i] = SideP::offset(wave + i * kWaves, lane, ldp, have_p);
-            cut_p[i] = SideP::offset(wave + i * kWaves, lane, ldp, have_p, left);
+            if constexpr (P_CUT)
+                cut_p[i] = SideP::offset(wave + i * kWaves, lane, ldp, have_p, left);
         }
 #pragma unroll
         for (int i = 0; i < kPerQ; ++i)
@@ -202,12 +210,19 @@ struct Product {
     // copy n of step s, to the slot `slot`
     __device__ __forceinline__ void copy(int n, int s, int slot, const uint8_t *p, const uint8_t *q)
     {
-        if (n < kPerP)
-            copy16<P_ONCE>(p, s == cut_step ? cut_p[n] : off_p[n],
-                   at_p + slot * SideP::kBytes + n * (kWaves * 1024));
+        const uint32_t to = at_p + slot * SideP::kBytes + n * (kWaves * 1024);
+        const bool cut = P_CUT && s == cut_step;
+        if (n < kPerP && P_ALONG && cut)
+            // zeros behind the row's end: what lies there is not the row's, and Q's zeros times
+            // an infinity would be no zeros
+            copy16(cut_p[n] == SideP::kNone ? reinterpret_cast<const uint8_t *>(kZeros)
+                                            : p + cut_p[n],
+                   to);
+        else if (n < kPerP)
+            copy16<P_ONCE>(p, cut ? cut_p[n] : off_p[n], to);
         else
             copy16<false>(q, off_q[n - kPerP],
-                   at_q + slot * SideQ::kBytes + (n - kPerP) * (kWaves * 1024));
+                          at_q + slot * SideQ::kBytes + (n - kPerP) * (kWaves * 1024));
     }
     // fragment n of a half: P's first, all of Q's, the rest of P's
     __device__ __forceinline__ void fragment(int n, int h, v8bf (&fp)[NP], v8bf (&fq)[NQ]) const

@@ -141,6 +141,25 @@ def test_rows_without_a_distribution(mxq_lib, rows):
     ref.check("dx", dx.cpu()[good], want.dx[good], want.d_dx[good])
 
 
+@pytest.mark.parametrize("rows", [3, 200])
+@pytest.mark.parametrize("hidden,at", [(32, 0), (32, 31), (96, 95), (64, 63), (160, 130)])
+def test_masked_logits(mxq_lib, rows, hidden, at):
+    """-inf and +inf in w, also where a step of the product goes on behind a row of it."""
+    d = dev()
+    x = torch.ones(rows, hidden).to(BF16)
+    w = torch.zeros(300, hidden).to(BF16)
+    w[::3, at] = -INF
+    targets = torch.arange(rows, dtype=torch.int32) * 3 % 300 + 1
+    loss, stats = mxq_lib.linear_ce_forward(x.to(d), w.to(d), targets.to(d))
+    assert stats.cpu().tolist() == [[0.0, 200.0]] * rows
+    assert torch.allclose(loss.cpu(), torch.log(torch.tensor(200.0)).expand(rows), rtol=1e-6)
+    dw = mxq_lib.linear_ce_backward(x.to(d), w.to(d), targets.to(d), stats, dx=False)[1].float().cpu()
+    assert not dw[::3].any() and (dw[2::3] > 0).all()
+    w[0, at] = INF
+    loss, stats = mxq_lib.linear_ce_forward(x.to(d), w.to(d), targets.to(d))
+    assert loss.isnan().all() and stats[:, 1].isnan().all()
+
+
 def test_masked_vocabulary(mxq_lib):
     """Logits of -inf: masked entries have q = 0; a row with nothing else has loss +inf, S = 0 and the
     gradient -weight / T at its target."""
