@@ -591,14 +591,21 @@ void with_logits(int64_t rows, int64_t hidden, int64_t vocab, F f)
         with_logits_of<ONCE, false>(rows, vocab, f);
 }
 // for dx, whose tiles are made enough by stretches of the vocabulary
-template <class F> void with_dx(int64_t rows, F f)
+template <bool CUT, class F> void with_dx_of(int64_t rows, F f)
 {
     if (rows <= 32)
-        f(Tag<Few<false, true, true>>{});
+        f(Tag<Few<false, true, CUT>>{});
     else if (rows <= 128)
-        f(Tag<Twin<false, true, true>>{});
+        f(Tag<Twin<false, true, CUT>>{});
     else
-        f(Tag<Many<false, true, true>>{});
+        f(Tag<Many<false, true, CUT>>{});
+}
+template <class F> void with_dx(int64_t rows, int64_t vocab, F f)
+{
+    if (vocab % kStepK)
+        with_dx_of<true>(rows, f);
+    else
+        with_dx_of<false>(rows, f);
 }
 // for dw
 template <class F> void with_dw(int64_t rows, int64_t hidden, int64_t vocab, F f)
@@ -657,7 +664,7 @@ BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws
     b.width = (int)width;
     b.ld = (int)pitch(width);
     b.dz = c.take<u16>(padded * b.ld);
-    with_dx(rows, [&](auto t) {
+    with_dx(rows, vocab, [&](auto t) {
         using Tile = typename decltype(t)::Tile;
         const int64_t np = tiles_of(hidden, Tile::kP), tiles = np * tiles_of(rows, Tile::kQ);
         b.fill = kCus * (Tile::kLds <= 65536 ? 2 : 1) * (rows <= 32 ? 2 : 1);
@@ -815,7 +822,7 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
     };
     const int n_dx = dx && rows > 0 ? (int)f.dx_groups : 0;
     with_logits<false>(rows, hidden, b.width, [&](auto tz) {
-        with_dx(rows, [&](auto tx) {
+        with_dx(rows, vocab, [&](auto tx) {
             with_dw(rows, hidden, b.width, [&](auto tw) {
                 using Logit = typename decltype(tz)::Tile;
                 using Dx = typename decltype(tx)::Tile;

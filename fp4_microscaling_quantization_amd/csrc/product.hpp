@@ -44,8 +44,7 @@ template <int ROWS, bool ALONG> struct Side {
 
     // What lane `lane` fetches for copy cc of a step, in bytes from the tile's first
     // element; ld in elements; rows past the last of `have` >= 1 fetch it again (their
-    // products are not used).  k past the last of `have_k`: kNone along k, else the last one
-    // again (their products are with zeros).
+    // products are not used).  kNone: k past the last of `have_k`.
     static constexpr uint32_t kNone = ~0u;
     static __device__ __forceinline__ uint32_t offset(int cc, int lane, int64_t ld, int have,
                                                       int have_k = kStepK)
@@ -60,7 +59,9 @@ template <int ROWS, bool ALONG> struct Side {
             constexpr int PER = ROWS / 8;  // chunks of one k
             const int k = cc * (64 / PER) + lane / PER;
             const int chunk = (lane % PER) ^ (2 * (k & 7));
-            return (uint32_t)(min(k, have_k - 1) * ld * 2 + min(chunk * 8, have - 8) * 2);
+            if (k >= have_k)
+                return kNone;
+            return (uint32_t)(k * ld * 2 + min(chunk * 8, have - 8) * 2);
         }
     }
 
@@ -211,15 +212,13 @@ struct Product {
     __device__ __forceinline__ void copy(int n, int s, int slot, const uint8_t *p, const uint8_t *q)
     {
         const uint32_t to = at_p + slot * SideP::kBytes + n * (kWaves * 1024);
-        const bool cut = P_CUT && s == cut_step;
-        if (n < kPerP && P_ALONG && cut)
-            // zeros behind the row's end: what lies there is not the row's, and Q's zeros times
-            // an infinity would be no zeros
+        if (n < kPerP && P_CUT && s == cut_step)
+            // zeros behind the last k: Q's zeros times an infinity would be no zeros
             copy16(cut_p[n] == SideP::kNone ? reinterpret_cast<const uint8_t *>(kZeros)
                                             : p + cut_p[n],
                    to);
         else if (n < kPerP)
-            copy16<P_ONCE>(p, cut ? cut_p[n] : off_p[n], to);
+            copy16<P_ONCE>(p, off_p[n], to);
         else
             copy16<false>(q, off_q[n - kPerP],
                           at_q + slot * SideQ::kBytes + (n - kPerP) * (kWaves * 1024));

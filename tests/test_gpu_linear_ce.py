@@ -160,6 +160,26 @@ def test_masked_logits(mxq_lib, rows, hidden, at):
     assert loss.isnan().all() and stats[:, 1].isnan().all()
 
 
+@pytest.mark.parametrize("rows", [3, 40, 200])
+@pytest.mark.parametrize("vocab", [33, 64, 321])
+def test_masked_target_behind_a_step(mxq_lib, rows, vocab):
+    """The vocabulary's last entry is masked by an infinity in w and is row 0's target: its dx there is
+    -1 times that infinity, the others' 0 times it."""
+    d = dev()
+    x = torch.ones(rows, 64).to(BF16)
+    w = torch.zeros(vocab, 64).to(BF16)
+    w[vocab - 1, 5] = -INF
+    targets = torch.zeros(rows, dtype=torch.int32)
+    targets[0] = vocab - 1
+    loss, stats = mxq_lib.linear_ce_forward(x.to(d), w.to(d), targets.to(d))
+    dx, _ = mxq_lib.linear_ce_backward(x.to(d), w.to(d), targets.to(d), stats, dw=False)
+    loss, dx = loss.cpu(), dx.float().cpu()
+    assert loss[0] == INF and loss[1:].isfinite().all()
+    assert dx[0, 5] == INF and dx[1:, 5].isnan().all()
+    dx[:, 5] = 0
+    assert not dx.any()
+
+
 def test_masked_vocabulary(mxq_lib):
     """Logits of -inf: masked entries have q = 0; a row with nothing else has loss +inf, S = 0 and the
     gradient -weight / T at its target."""
