@@ -23,7 +23,10 @@ constexpr int kThreads = 256;
 constexpr int kMostTensors = 1024;  // of a launch: 28 KB of arguments
 constexpr int64_t kTypeBit = int64_t(1) << 62, kOutBit = int64_t(1) << 61;  // set: bf16
 constexpr int64_t kCached = int64_t(192) << 20;  // bytes that stay in the last-level cache
-constexpr int64_t kMostElements = int64_t(1) << 48;
+// elements of a list (more than the memory holds), and workgroups of a launch: its threads are
+// counted in 32 bits
+constexpr int64_t kMostElements = int64_t(1) << 38;
+constexpr int64_t kMostGroups = int64_t(1) << 23;
 
 template <int N> struct Batch {
     const void *g[N];
@@ -264,7 +267,7 @@ void for_batches_of(const mxq_grad *grads, int64_t count, int chunk, F launch)
         if (g.n == 0)
             continue;
         const int64_t need = (g.n + chunk - 1) / chunk;
-        if (b.count == N || (b.count > 0 && groups + need > INT32_MAX))
+        if (b.count == N || (b.count > 0 && groups + need > kMostGroups))
             flush();
         b.g[b.count] = g.g;
         b.out[b.count] = g.out;

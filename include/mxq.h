@@ -458,9 +458,8 @@ mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t ro
 
 /* ---- the ends of a training step --------------------------------------------
  * Softmax cross entropy of an output layer from its hidden states and weight,
- * a piece of the vocabulary at a time: the logits z = x w^T are never kept, so
- * the workspaces do not grow with rows x vocab.  With q = softmax(z / temperature)
- * and weight[r] (fp32 [rows], NULL: 1),
+ * a piece of the vocabulary at a time: the logits z = x w^T are never kept.
+ * With q = softmax(z / temperature) and weight[r] (fp32 [rows], NULL: 1),
  *   loss[r]  = -weight[r] log q at targets[r];
  *   stats[r] = (m, S) as mxq_token_logprobs writes them, S = sum exp((z - m) / temperature);
  *   dz       = weight[r] / temperature (q - 1[v = target]),
@@ -483,7 +482,9 @@ mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t ro
  *  - rows == 0: the forward pass does nothing, the backward pass clears dw.
  *  - dx or dw may be NULL.  No output may overlap an input.
  * workspace: 16-byte aligned, of the size that the functions below give (0 for
- * sizes that are refused). */
+ * sizes that are refused): the rows that count, packed; with them for the forward
+ * pass 8 bytes for each row and 128 or 256 entries of the vocabulary, for the
+ * backward pass dz of a piece (256 MiB and a part) and the sums of dx in fp32. */
 mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const void *w, int64_t ld_w,
                                  int64_t rows, int64_t hidden, int64_t vocab, float temperature,
                                  const int32_t *targets, const float *weight, float *loss,
@@ -510,9 +511,9 @@ size_t mxq_linear_ce_backward_workspace_size(int64_t rows, int64_t hidden, int64
  *    then to bf16 where out is.  Where c is 1, out is g; out == g is then left alone.
  *  - A norm that is infinite gives c = 0, one that is NaN c = NaN, in IEEE
  *    arithmetic (infinities become NaN, and everything does).
- *  - Empty tensors and empty lists serve (norm 0).  An out may overlap no other
- *    tensor's g or out.  max_norm and eps are finite and >= 0; where max_norm,
- *    norm and eps are all 0, c is NaN.
+ *  - Empty tensors and empty lists serve (norm 0); a list has at most 2^38
+ *    elements.  An out may overlap no other tensor's g or out.  max_norm and
+ *    eps are finite and >= 0; where max_norm, norm and eps are all 0, c is NaN.
  *  - mxq_grad_norm only reads g, n and dtype.
  * workspace: mxq_grad_norm_workspace_size(grads, count) bytes, 8-byte aligned (0
  * for empty lists and those that are refused). */

@@ -81,6 +81,17 @@ def test_grad_norm_refusals(mxq_lib):
     assert f(good, ws=None) == f(good, size=7) == f(good, (B, None, 10, 1, 0), size=8) == m.ERR_WORKSPACE
 
 
+def test_most_elements(mxq_lib):
+    """Above any memory, and within what a launch counts its workgroups in."""
+    m, L = mxq_lib, mxq_lib.lib()
+    most = 1 << 38
+    assert L.mxq_grad_norm_workspace_size(*grads_of(m, (A, None, most, 1, 0))) == 8 * (most // 32768)
+    for list_ in [((A, None, most + 1, 1, 0),), ((A, None, most, 0, 0), (B, None, 1, 0, 0))]:
+        arr, n = grads_of(m, *list_)
+        assert L.mxq_grad_norm_workspace_size(arr, n) == 0
+        assert L.mxq_grad_norm(arr, n, D, E, F, 1 << 40, None) == m.ERR_SHAPE
+
+
 def test_grad_clip_refusals(mxq_lib):
     m, L = mxq_lib, mxq_lib.lib()
 
