@@ -41,7 +41,9 @@ struct CePacked {
 
 __device__ __forceinline__ bool row_counts(const CeRows &a, int64_t r)
 {
-    return a.targets[r] >= 0 && !(a.weight && a.weight[r] == 0.0f);
+    const int target = a.targets[r];
+    const float weight = a.weight ? a.weight[r] : 1.0f;  // both are on their way
+    return (target >= 0) & (weight != 0.0f);
 }
 
 // dz is rounded to bf16.  With all weights alike, and most q small, most of its entries at a
@@ -98,6 +100,7 @@ __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per,
     const int64_t first = behind ? a.rows : (int64_t)blockIdx.x * per;
     const int64_t end = first + per < a.rows ? first + per : a.rows;
     int place = 0;
+#pragma unroll 8
     for (int64_t r = threadIdx.x; r < first; r += kPackThreads)
         place += row_counts(a, r);
     place = block_count(place);
@@ -251,8 +254,8 @@ __global__ __launch_bounds__(256) void k_ce_loss(CeRows a, CePacked x, int vocab
                                                  const float2 *part, int64_t stride, Heat heat,
                                                  float *loss, float2 *stats)
 {
-    constexpr int K = 256 / ROWS;  // threads of a row
-    __shared__ float2 joint[K][ROWS];
+    constexpr int K = 256 / ROWS, WAVES = 4;  // threads of a row
+    __shared__ float2 joint[WAVES][ROWS];
     const int r = threadIdx.x % ROWS, k = threadIdx.x / ROWS;
     const int64_t row = (int64_t)blockIdx.x * ROWS + r;
     int at = -1;
@@ -275,15 +278,16 @@ __global__ __launch_bounds__(256) void k_ce_loss(CeRows a, CePacked x, int vocab
             join_stats(st, part[(int64_t)i * stride + at], heat.log2);
     }
 #pragma unroll
-    for (int to = K / 2; to > 0; to /= 2) {
-        joint[k][r] = make_float2(st.m, st.s);
-        __syncthreads();
-        if (k < to)
-            join_stats(st, joint[k + to][r], heat.log2);
-        __syncthreads();
-    }
+    for (int d = ROWS; d < 64; d *= 2)
+        join_stats(st, make_float2(__shfl_xor(st.m, d), __shfl_xor(st.s, d)), heat.log2);
+    if ((threadIdx.x & 63) < ROWS)
+        joint[threadIdx.x >> 6][r] = make_float2(st.m, st.s);
+    __syncthreads();
     if (k > 0 || row >= a.rows)
         return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w)
+        join_stats(st, joint[w][r], heat.log2);
     if (at < 0) {
         loss[row] = 0.0f;
         stats[row] = make_float2(0.0f, 1.0f);
