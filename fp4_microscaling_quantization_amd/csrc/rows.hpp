@@ -64,6 +64,14 @@ __device__ __forceinline__ void unpack(gv4u raw, float (&f)[8], bf16_t *)
         f[2 * j + 1] = as_f(raw[j] & 0xFFFF0000u);
     }
 }
+__device__ __forceinline__ void unpack(gv2u raw, float (&f)[4], bf16_t *)
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        f[2 * j] = as_f(raw[j] << 16);
+        f[2 * j + 1] = as_f(raw[j] & 0xFFFF0000u);
+    }
+}
 __device__ __forceinline__ void unpack(gv4u raw, float (&f)[4], float *)
 {
 #pragma unroll
