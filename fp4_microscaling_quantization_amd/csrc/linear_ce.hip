@@ -157,6 +157,12 @@ using Twin = Product<4, 1, 2, 8, 2, P_ALONG, Q_ALONG, CUT, ONCE>;  // 128 x 128
 // three or four steps in LDS, 69 with two.)
 template <bool P_ALONG, bool Q_ALONG, bool CUT, bool ONCE = false>
 using Few = Product<4, 1, 2, 2, 3, P_ALONG, Q_ALONG, CUT, ONCE>;  // 128 x 32
+// Products of so few tiles that each has a CU, or half of one, to itself: what they take is the
+// time of their steps one after another, and a smaller tile's are shorter.
+template <bool P_ALONG, bool Q_ALONG, bool CUT, bool ONCE = false>
+using Small = Product<2, 2, 2, 2, 4, P_ALONG, Q_ALONG, CUT, ONCE>;  // 64 x 64
+template <bool P_ALONG, bool Q_ALONG, bool CUT, bool ONCE = false>
+using Slim = Product<4, 1, 1, 2, 6, P_ALONG, Q_ALONG, CUT, ONCE>;  // 64 x 32
 // dw of rows that are one step of the product over them
 using Outer = Product<2, 2, 4, 4, 1, false, false, false>;  // 128 x 128
 
@@ -572,10 +578,17 @@ constexpr int64_t kPieceLogits = MXQ_PIECE_LOGITS;
 // 4096 x 128256 in the forward pass 205 us without the hint, 182 with it).
 template <bool ONCE, bool CUT, class F> void with_logits_of(int64_t rows, int64_t vocab, F f)
 {
-    // 100 rows under 32000 x 4096 (250 tiles) Deep 64 us, Twin 78; under 128256 x 4096 222 and 203;
-    // 200 rows under 32000 x 4096 (125 tiles) Half 79 us, Many 126; 400 rows (250) 153 and 135
-    if (rows <= 32)
+    // Forward passes: 4 rows under 8000 x 4096 (125 tiles) Slim 21 us, Few 34; 16 under 32003 x 4096
+    // (501) 56 and 50.  100 rows under 8000 x 4096 (250) Small 36 us, Deep 42; under 16000 (500) 64
+    // and 49.  200 under 8000 x 4096 (500) Small 58, Half 68; 300 (625) 77 and 64.  100 under 32000 x 4096 (250) Deep 64 us, Twin 78; under 128256 222 and 203.
+    // 200 under 32000 x 4096 (125) Half 79 us, Many 126; 400 (250) 153 and 135.
+    const int64_t small = tiles_of(vocab, 64) * tiles_of(rows, 64);
+    if (rows <= 32 && small <= kCus)
+        f(Tag<Slim<true, true, CUT, ONCE>>{});
+    else if (rows <= 32)
         f(Tag<Few<true, true, CUT, ONCE>>{});
+    else if (small <= (rows <= 128 ? kCus : 2 * kCus))
+        f(Tag<Small<true, true, CUT, ONCE>>{});
     else if (rows <= 128 && tiles_of(vocab, 128) <= kCus)
         f(Tag<Deep<true, true, CUT, ONCE>>{});
     else if (rows <= 128)
@@ -594,22 +607,29 @@ void with_logits(int64_t rows, int64_t hidden, int64_t vocab, F f)
     else
         with_logits_of<ONCE, false>(rows, vocab, f);
 }
-// for dx, whose tiles are made enough by stretches of the vocabulary
-template <bool CUT, class F> void with_dx_of(int64_t rows, F f)
+// for dx, whose tiles are made enough by stretches of the vocabulary, where it is long enough
+constexpr int kStretch = 512;
+int64_t most_stretches(int64_t width) { return width / kStretch > 0 ? width / kStretch : 1; }
+template <bool CUT, class F> void with_dx_of(int64_t rows, int64_t hidden, int64_t width, F f)
 {
+    // backward passes of 200 rows under 1000 x 4096 (16 tiles of all stretches) Deep 70 us, Many 80;
+    // 1024 under 16000 x 512 (248) 88 and 95; 200 under 16000 x 4096 (496) 174 and 172; 800 under
+    // 16000 x 4096 (1984) 376 and 337
     if (rows <= 32)
         f(Tag<Few<false, true, CUT>>{});
     else if (rows <= 128)
         f(Tag<Twin<false, true, CUT>>{});
+    else if (tiles_of(hidden, 256) * tiles_of(rows, 256) * most_stretches(width) <= kCus)
+        f(Tag<Deep<false, true, CUT>>{});
     else
         f(Tag<Many<false, true, CUT>>{});
 }
-template <class F> void with_dx(int64_t rows, int64_t vocab, F f)
+template <class F> void with_dx(int64_t rows, int64_t hidden, int64_t width, int64_t vocab, F f)
 {
     if (vocab % kStepK)
-        with_dx_of<true>(rows, f);
+        with_dx_of<true>(rows, hidden, width, f);
     else
-        with_dx_of<false>(rows, f);
+        with_dx_of<false>(rows, hidden, width, f);
 }
 // for dw
 template <class F> void with_dw(int64_t rows, int64_t hidden, int64_t vocab, F f)
@@ -668,11 +688,11 @@ BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws
     b.width = (int)width;
     b.ld = (int)pitch(width);
     b.dz = c.take<u16>(padded * b.ld);
-    with_dx(rows, vocab, [&](auto t) {
+    with_dx(rows, hidden, width, vocab, [&](auto t) {
         using Tile = typename decltype(t)::Tile;
         const int64_t np = tiles_of(hidden, Tile::kP), tiles = np * tiles_of(rows, Tile::kQ);
         b.fill = kCus * (Tile::kLds <= 65536 ? 2 : 1) * (rows <= 32 ? 2 : 1);
-        b.room = (int)(width / 512 > 0 ? width / 512 : 1);
+        b.room = (int)most_stretches(width);
         // slabs x tiles are at most `fill` where there is more than one slab
         const int64_t slab_rows = Tile::kQ * (b.fill / np);
         const int64_t all = slab_rows < b.room * rows ? slab_rows : b.room * rows;
@@ -760,10 +780,9 @@ extern "C" mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const v
     with_logits<true>(rows, hidden, vocab, [&](auto t) {
         using Tile = typename decltype(t)::Tile;
         const int64_t groups = f.tiles * tiles_of(rows, Tile::kQ);
-        // Rows that are all of one tile are read where they are, if they can be: the ones that do
-        // not count cost nothing there, and packing a launch (one row under 32000 x 1024 19 us
-        // with it, 15 without).
-        if (rows <= Tile::kQ && rows <= 128 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
+        // Few rows are read where they are, if they can be: the ones that do not count cost little
+        // there, and packing a launch (one row under 32000 x 1024 19 us with it, 15 without).
+        if (rows <= 128 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
             ld_x % 8 == 0 && hidden % kStepK == 0 && ld_x <= kMostLd) {
             f.x.all = (int)rows;
             f.x.x = const_cast<u16 *>(static_cast<const u16 *>(x));
@@ -826,7 +845,7 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
     };
     const int n_dx = dx && rows > 0 ? (int)f.dx_groups : 0;
     with_logits<false>(rows, hidden, b.width, [&](auto tz) {
-        with_dx(rows, vocab, [&](auto tx) {
+        with_dx(rows, hidden, b.width, vocab, [&](auto tx) {
             with_dw(rows, hidden, b.width, [&](auto tw) {
                 using Logit = typename decltype(tz)::Tile;
                 using Dx = typename decltype(tx)::Tile;

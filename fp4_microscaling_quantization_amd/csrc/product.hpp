@@ -341,14 +341,15 @@ struct Product {
         barrier_no_fence();
     }
     // The tile in bf16 through the LDS, so that it leaves as whole lines: put() every
-    // acc[i][j], packed, then flush().  16-byte chunk c of row q lies at c ^ (q & 15).
+    // acc[i][j], packed, then flush().  16-byte chunk c of row q lies at c ^ q, of up to 16 chunks.
     static_assert(kP * kQ * 2 <= kLds, "the tile in bf16 fits where its operands were");
+    static constexpr int kSwap = (kP < 128 ? kP / 8 : 16) - 1;
     __device__ __forceinline__ void put(uint8_t *lds, int i, int j, gv2u packed) const
     {
         const int p = p_of(i), q = q_of(j);
         typedef __attribute__((address_space(3))) gv2u lds_gv2u;
         *(lds_gv2u *)(__attribute__((address_space(3))) uint8_t *)(
-            lds + q * (kP * 2) + ((p >> 3) ^ (q & 15)) * 16 + (p & 4) * 2) = packed;
+            lds + q * (kP * 2) + ((p >> 3) ^ (q & kSwap)) * 16 + (p & 4) * 2) = packed;
     }
     // its first `rows` rows of q and `cols` (a multiple of 8) of p; ONCE: not read again
     template <bool ONCE>
@@ -364,7 +365,7 @@ struct Product {
         for (int q = threadIdx.x / WIDE; q < kQ; q += kThreads / WIDE) {
             typedef __attribute__((address_space(3))) const gv4u lds_gv4u;
             const gv4u v = *(lds_gv4u *)(__attribute__((address_space(3))) const uint8_t *)(
-                lds + q * (kP * 2) + (c ^ (q & 15)) * 16);
+                lds + q * (kP * 2) + (c ^ (q & kSwap)) * 16);
             if (q < rows) {
                 MXQ_GLOBAL gv4u *at = (MXQ_GLOBAL gv4u *)(to + (int64_t)q * ld + c * 8);
                 if constexpr (ONCE)
