@@ -8,6 +8,10 @@
 // clipping.  The squares are summed in fp64, where they are exact and neither overflow
 // nor vanish; its two instructions an element hide behind the loads.
 //
+// 2.0 GB of bf16: norm 298 us, 6.7 TB/s.  5.6 GB of fp32 to bf16: norm 0.80 ms (6.9 TB/s),
+// clipping 1.53 (5.5).  700 tensors, 91 MB in both: 32 us, bound by launches and by finding
+// and starting on short tensors.
+//
 // The list goes to the kernels as an argument (no table in device memory that would have
 // to be copied there, or be kept), a batch of it a launch.  A workgroup takes one chunk of
 // one tensor, and finds it by counting the tensors that start at or before it.  The

@@ -9,6 +9,12 @@
 //             products dx += dz w and dw = dz^T x then read.
 //
 // Rows that do not count are left out of all of it: the rows that do are packed first.
+//
+// Few rows are bound by the weight's bytes, many by the matrix cores.  24 rows under
+// 128256 x 4096: forward 183 us, 5.7 TB/s.  16 under 32003 x 4096: backward 167 us, of it
+// dz 40 (6.6 TB/s), dx 43, dw 60 (written at 4.4).  8192 rows, of which 7373 count, under
+// 128256 x 4096: forward 5.5 ms (1.40 PF); backward 17.7 ms, of it dz 5.8 (1.34 PF), dx 6.2
+// (1.25), dw 5.5 (1.41), packing, sums and the join of dx 0.1.
 #include "product.hpp"
 #include "rows.hpp"
 #include "vocab.hpp"
@@ -337,7 +343,8 @@ __device__ __forceinline__ int slabs_of(int tiles, int fill, int room)
 
 // Tile `at` of the piece's dz, [rows][ld] in bf16; zero behind the last row (up to the
 // tile's end, and a whole step) and the last of the vocabulary.
-template <class Tile> __device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int piece, int at)
+template <class Tile>
+__device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int piece, int at)
 {
     const int count = *b.x.count;
     const int np = (b.have(piece) + Tile::kP - 1) / Tile::kP;
@@ -408,7 +415,8 @@ template <class Tile> __device__ __forceinline__ void dlogits(uint8_t *lds, cons
 }
 
 // Tile `at` of all slabs' for dx = dz w, added to (for the first piece, written as) the sums.
-template <class Tile> __device__ __forceinline__ void dx_part(uint8_t *lds, const Backward &b, int piece, int at)
+template <class Tile>
+__device__ __forceinline__ void dx_part(uint8_t *lds, const Backward &b, int piece, int at)
 {
     const int count = *b.x.count;
     const int np = (b.w.hidden + Tile::kP - 1) / Tile::kP, nq = (count + Tile::kQ - 1) / Tile::kQ;
@@ -425,7 +433,8 @@ template <class Tile> __device__ __forceinline__ void dx_part(uint8_t *lds, cons
     const int have = b.have(piece) - v0;  // of the stretch's vocabulary, to the piece's end
     const int n = max(0, min(steps, (have + kStepK - 1) / kStepK));
     Tile t;
-    const uint8_t *p = reinterpret_cast<const uint8_t *>(b.w.w + (int64_t)(b.first(piece) + v0) * b.w.ld + p0);
+    const uint8_t *p =
+        reinterpret_cast<const uint8_t *>(b.w.w + (int64_t)(b.first(piece) + v0) * b.w.ld + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(b.dz + (int64_t)q0 * b.ld + v0);
     // dz is zero behind the vocabulary's last
     t.start(lds, b.w.ld, b.w.hidden - p0, b.ld, Tile::kQ, max(0, have));
@@ -444,7 +453,8 @@ template <class Tile> __device__ __forceinline__ void dx_part(uint8_t *lds, cons
 }
 
 // Tile `at` of dw = dz^T x of the piece's vocabulary.
-template <class Tile> __device__ __forceinline__ void dw_part(uint8_t *lds, const Backward &b, int piece, int at)
+template <class Tile>
+__device__ __forceinline__ void dw_part(uint8_t *lds, const Backward &b, int piece, int at)
 {
     const int np = (b.w.hidden + Tile::kP - 1) / Tile::kP;
     const int have = b.have(piece);
@@ -485,7 +495,8 @@ __global__ __launch_bounds__(Tile::kThreads, 1) void k_ce_dx(Backward b, int pie
     dx_part<Tile>(lds, b, piece, blockIdx.x);
 }
 template <class Tile>
-__global__ __launch_bounds__(Tile::kThreads, Tile::kLds <= 32768 ? 4 : 1) void k_ce_dw(Backward b, int piece)
+__global__ __launch_bounds__(Tile::kThreads, Tile::kLds <= 32768 ? 4 : 1) void k_ce_dw(Backward b,
+                                                                                     int piece)
 {
     __shared__ __align__(16) uint8_t lds[Tile::kLds];
     dw_part<Tile>(lds, b, piece, blockIdx.x);
@@ -580,8 +591,9 @@ template <bool ONCE, bool CUT, class F> void with_logits_of(int64_t rows, int64_
 {
     // Forward passes: 4 rows under 8000 x 4096 (125 tiles) Slim 21 us, Few 34; 16 under 32003 x 4096
     // (501) 56 and 50.  100 rows under 8000 x 4096 (250) Small 36 us, Deep 42; under 16000 (500) 64
-    // and 49.  200 under 8000 x 4096 (500) Small 58, Half 68; 300 (625) 77 and 64.  100 under 32000 x 4096 (250) Deep 64 us, Twin 78; under 128256 222 and 203.
-    // 200 under 32000 x 4096 (125) Half 79 us, Many 126; 400 (250) 153 and 135.
+    // and 49.  200 under 8000 x 4096 (500) Small 58, Half 68; 300 (625) 77 and 64.  100 under
+    // 32000 x 4096 (250) Deep 64 us, Twin 78; under 128256 222 and 203.  200 under 32000 x 4096
+    // (125) Half 79 us, Many 126; 400 (250) 153 and 135.
     const int64_t small = tiles_of(vocab, 64) * tiles_of(rows, 64);
     if (rows <= 32 && small <= kCus)
         f(Tag<Slim<true, true, CUT, ONCE>>{});
@@ -858,7 +870,8 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
                 };
                 const auto launch = [&](auto kernel, int threads, int64_t groups, auto... args) {
                     if (groups > 0)
-                        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), 0, s, b, args...);
+                        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), 0, s, b,
+                                           args...);
                 };
                 for (int i = 0; i < (int)f.pieces; ++i) {
                     launch(k_ce_dlogits<Logit>, Logit::kThreads, n_z(i), i);

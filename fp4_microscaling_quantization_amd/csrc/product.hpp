@@ -18,7 +18,17 @@
 // Both are copied as they lie, 16 bytes a lane, into LDS.  A lane's place in LDS is
 // fixed (16 bytes times its number), so the order within a tile is made by what each
 // lane fetches: 16-byte chunks are exchanged within a row (chunk c of row r lies at
-// c ^ x(r)) so that the 16 lanes that read at a time touch every bank once.
+// c ^ x(r)) so that the 16 lanes that read at a time touch every bank once.  (The 32 lanes
+// of two groups that read across k meet in half of the banks, and half of those reads' LDS
+// cycles wait.  An exchange that takes the group's bit too leaves none of them, and the
+// backward pass below takes 17.72 ms with it, 17.67 without.)
+//
+// What bounds it: the matrix cores, and the power that they take.  256 x 256 tiles take
+// 1.4 us a step of 64 k and 7.5 us a tile besides (its start, its epilogue): 1.38 to
+// 1.43 PF over 4096 k, 1.65 and more when the operands are zeros.  In 8192 x 4096 x 16384
+// the matrix cores are busy for 72 to 76% of the cycles, at 2.0 GHz of 2.4.  A read or a
+// copy between every few products takes their waits out: all copies first are 2% slower, all
+// last 5%.
 #pragma once
 
 #include <type_traits>
