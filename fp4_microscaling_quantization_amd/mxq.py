@@ -806,7 +806,8 @@ def _grad_list(grads, out=None, write=True):
 def prepare_grad_norm(grads):
     """grad_norm(grads) marshalled once: a function that launches it on the current
     stream (or `stream`) again and returns the same (norm, sum_sq) tensors.  It
-    holds the gradients and a workspace; calls of it that overlap race."""
+    holds the gradients and a workspace, made on the stream that is current here;
+    calls of it that overlap race."""
     arr, keep = _grad_list(grads, write=False)
     first = keep[0][0]
     torch, _ = _enter(first, None)
@@ -826,7 +827,8 @@ def prepare_grad_norm(grads):
 def prepare_clip_grad_norm(grads, max_norm, *, eps, out=None):
     """clip_grad_norm(grads, max_norm) marshalled once: a function that launches it
     on the current stream (or `stream`) again and returns the same norm tensor.  It
-    holds the gradients, the outputs and a workspace; calls of it that overlap race."""
+    holds the gradients, the outputs and a workspace, made on the stream that is
+    current here; calls of it that overlap race."""
     arr, keep = _grad_list(grads, out)
     first = keep[0][0]
     measure = prepare_grad_norm(keep[0])
