@@ -11,8 +11,9 @@ from test_gpu_linear_ce_exact import case as exact_case, check_forward, given, g
 
 pytestmark = pytest.mark.gpu
 
-# rows, hidden, vocab: few rows; up to 128; more.  A hidden size that ends within a step, and one that does not.
-SHAPES = [(20, 96, 16385), (32, 64, 16448), (100, 96, 8321), (70, 64, 8192 + 64), (128, 96, 32833), (100, 64, 33024),
+# rows, hidden, vocab: small tiles over rows that are not packed; few rows; up to 128; more.  A hidden size that ends
+# within a step, and one that does not.
+SHAPES = [(33, 64, 700), (65, 128, 300), (128, 64, 1000), (20, 96, 16385), (32, 64, 16448), (100, 96, 8321), (70, 64, 8192 + 64), (128, 96, 32833), (100, 64, 33024),
           (200, 96, 8257), (256, 64, 8320), (600, 96, 11077), (530, 64, 11136), (600, 288, 16451), (513, 320, 16512), (700, 288, 23045)]
 
 
