@@ -48,6 +48,11 @@ __device__ __forceinline__ void dma16_so(const uint8_t *base, uint32_t off, cons
                  : "memory");
 }
 
+__device__ __forceinline__ uint32_t lds_address(const void *l)
+{
+    return (uint32_t)(uintptr_t)((__attribute__((address_space(3))) const void *)l);
+}
+
 // The same to an LDS address held in a scalar register.  ONCE: what is not read again leaves
 // the caches to what is.
 template <bool ONCE>

@@ -6,7 +6,8 @@
 //             and a second kernel joins them over the tiles.
 //   backward  a piece of the vocabulary at a time: the product again, turned into
 //             dz = weight / T (exp((z - m) / T) / s - 1[v = target]) in bf16, which the two
-//             products dx += dz w and dw = dz^T x then read.
+//             products dx += dz w and dw = dz^T x then read; what the rounding of dz left at
+//             the targets is added to both.
 //
 // Rows that do not count are left out of all of it: the rows that do are packed first.
 //
@@ -40,7 +41,6 @@ struct CePacked {
     int *place;        // [rows]: a row's place among them, -1: none
     int *row;          // [count]
     float *at_target;  // [count]: the logit at the target
-    float *unit;       // what dz is divided by, see unit_of
     u16 *x;            // [count, up to a whole step][ld], zero behind both
     int ld;            // hidden, up to a whole step
 };
@@ -52,16 +52,22 @@ __device__ __forceinline__ bool row_counts(const CeRows &a, int64_t r)
     return (target >= 0) & (weight != 0.0f);
 }
 
-// dz is rounded to bf16.  With all weights alike, and most q small, most of its entries at a
-// target are near -weight / T: rounded as they are, they would all be off by the same up to
-// 0.4%, and dx and dw with them.  So dz leaves out the significand of the first row's
-// weight / T, in [1, 2), and dx and dw are multiplied by it in fp32: entries near -2^e are off
-// by what their own q makes of them (1351 rows under 50257 x 1600 at a temperature of 0.7: dx
-// and dw are off by 0.31% in the mean without it, 0.19% with it, 0.17% of it their own rounding).
-__device__ __forceinline__ float unit_of(float scale)
+// dz is rounded to bf16 for the products behind it.  The largest entry of most rows is the one
+// at the target, near -weight / T: its rounding would be most of what is off in dx and dw, and
+// with all weights alike and most q small it would be off by the same up to 0.4% in every row.  So
+// what that one entry's rounding left is kept in fp32, and its part of dx and dw is added to their
+// sums.  (1351 rows under 50257 x 1600 at a temperature of 0.7: dx and dw are off by 0.31% in the mean
+// without it, by 0.17% with it, as fp32 products are: it is their own rounding.  It takes 8 us of 685, and
+// of 17.7 ms for 7373 rows under 128256 x 4096 less than can be told.)
+__device__ __forceinline__ float rounding_left(float d)
 {
-    const uint32_t u = as_u(scale), e = u >> 23 & 255;
-    return e == 0 || e == 255 ? 1.0f : as_f((u & 0x7FFFFF) | 0x3F800000);
+    const float stored = (float)(bf16_t)d;
+    return fabsf(stored) < INFINITY ? d - stored : 0.0f;
+}
+// rest times a value of the other operand.  The rounded entry's product has the infinities and NaN.
+__device__ __forceinline__ float rest_of(float rest, float other)
+{
+    return fabsf(other) < INFINITY ? rest * other : 0.0f;
 }
 
 // the statistics of two stretches of a row, as one
@@ -92,16 +98,102 @@ __device__ __forceinline__ int block_count(int n)
     return n;
 }
 
+// Rows by their targets, for what Rests adds to dw: those with their target in a tile of dw are
+// neighbours in a list, in order.  A workgroup makes one tile's part: it counts all rows, those in
+// the tile and those in front of it, a quarter of the rows a wave, then goes through them once more.
+// A row whose target is beyond the vocabulary is in no list, and one with every logit masked is not
+// either: it may hold infinities, which times the zeros of other entries would be none.  (x of the others is
+// finite: an infinity there makes every logit infinite, and the row has no distribution.)
+struct CeTargets {
+    int tiles, shift, vocab;  // of dw, 1 << shift entries wide
+    const float2 *stats;
+    int *rows, *starts;
+};
+__device__ __forceinline__ void list_targets(const CeRows &a, const CeTargets &to, int tile)
+{
+    constexpr int WAVES = kPackThreads / 64;
+    __shared__ int sums[3][WAVES];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t part = (a.rows + WAVES * 64 - 1) / (WAVES * 64) * 64;
+    const int64_t first = wave * part, end = first + part < a.rows ? first + part : a.rows;
+    const uint64_t below = (1ull << lane) - 1;
+    int counts = 0, here = 0, before = 0;
+    // f(which of 64 rows count, are in the tile, are in front of it), `ahead` times 64 rows in flight
+    const auto go_by = [&](auto ahead, auto f) {
+        constexpr int AHEAD = decltype(ahead)::value;
+        for (int64_t base = first; base < end; base += AHEAD * 64) {
+            int target[AHEAD];
+            float weight[AHEAD], s[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int64_t at = base + u * 64 + lane, r = at < end ? at : end - 1;
+                target[u] = at < end ? a.targets[r] : -1;
+                weight[u] = a.weight ? a.weight[r] : 1.0f;
+                s[u] = to.stats[r].y;
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const bool in = (target[u] >= 0) & (weight[u] != 0.0f);
+                const bool ok = in & (target[u] < to.vocab) & (s[u] != 0.0f);
+                f(__ballot(in), __ballot(ok && target[u] >> to.shift == tile),
+                  __ballot(ok && target[u] >> to.shift < tile));
+            }
+        }
+    };
+    const auto go = [&](auto f) {
+        if (part == 64)
+            go_by(std::integral_constant<int, 1>{}, f);
+        else
+            go_by(std::integral_constant<int, 4>{}, f);
+    };
+    go([&](uint64_t in, uint64_t mine, uint64_t front) {
+        counts += __popcll(in);
+        here += __popcll(mine);
+        before += __popcll(front);
+    });
+    if (lane == 0) {
+        sums[0][wave] = counts;
+        sums[1][wave] = here;
+        sums[2][wave] = before;
+    }
+    __syncthreads();
+    int start = 0, all = 0;
+    counts = here = 0;
+    for (int w = 0; w < WAVES; ++w) {
+        start += sums[2][w];
+        all += sums[1][w];
+        counts += w < wave ? sums[0][w] : 0;
+        here += w < wave ? sums[1][w] : 0;
+    }
+    if (threadIdx.x == 0) {
+        to.starts[tile] = start;
+        if (tile == to.tiles - 1)
+            to.starts[tile + 1] = start + all;
+    }
+    if (all == 0)
+        return;
+    go([&](uint64_t in, uint64_t mine, uint64_t) {
+        if (mine >> lane & 1)
+            to.rows[start + here + __popcll(mine & below)] = counts + __popcll(in & below);
+        counts += __popcll(in);
+        here += __popcll(mine);
+    });
+}
+
 // The rows that count, in order: where each went (or -1), which it was, how many, and
 // their values, with zeros behind the last value up to a whole step.  A workgroup takes
-// `per` rows, and finds their place by counting all rows in front of them.  The ones
+// `per` rows, and finds their place by counting all rows in front of them.  The kStepK - 1
 // behind `groups` write zeros behind the last row up to a whole step, which the product
-// over the rows reads, a row each.
+// over the rows reads, a row each.  The ones behind those list rows by their targets (list_targets).
 __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per, int groups,
                                                           const bf16_t *x, int64_t ld, int hidden,
-                                                          float inv_t, CePacked to)
+                                                          CePacked to, CeTargets lists)
 {
     const int lane = threadIdx.x & 63;
+    if ((int)blockIdx.x >= groups + kStepK - 1) {
+        list_targets(a, lists, (int)blockIdx.x - (groups + kStepK - 1));
+        return;
+    }
     const bool behind = (int)blockIdx.x >= groups;
     const int64_t first = behind ? a.rows : (int64_t)blockIdx.x * per;
     const int64_t end = first + per < a.rows ? first + per : a.rows;
@@ -127,8 +219,6 @@ __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per,
             to.place[mine] = in ? at : -1;
             if (in)
                 to.row[at] = (int)mine;
-            if (in && at == 0)
-                *to.unit = unit_of((a.weight ? a.weight[mine] : 1.0f) * inv_t);
         }
         int n = place;
         for (uint64_t left = all; left; left &= left - 1, ++n) {
@@ -139,11 +229,8 @@ __global__ __launch_bounds__(kPackThreads) void k_ce_pack(CeRows a, int64_t per,
         }
         place += __popcll(all);
     }
-    if ((int)blockIdx.x == groups - 1 && threadIdx.x == 0) {
+    if ((int)blockIdx.x == groups - 1 && threadIdx.x == 0)
         *to.count = place;
-        if (place == 0)
-            *to.unit = 1.0f;
-    }
 }
 
 // ---- logits ----------------------------------------------------------------------
@@ -320,10 +407,13 @@ struct Backward {
     CePacked x;
     Heat heat;
     const float2 *stats;
-    int width, ld;  // of dz
-    u16 *dz;        // of a piece, [rows][ld]
-    float *sums;    // slabs of [count][hidden]
-    int fill, room; // workgroups that fill the chip, and most slabs
+    int width, ld;   // of dz
+    u16 *dz;         // of a piece, [rows][ld]
+    int *by_target;  // [count]: packed rows by their targets' tiles of dw, in order within each
+    int *starts;     // [tiles and one]: where in it a tile's begin
+    int4 *left;      // [count]: a row's target, and what the rounding of dz left there (fp32)
+    float *sums;     // slabs of [count][hidden]
+    int fill, room;  // workgroups that fill the chip, and most slabs
     u16 *dw;
     int64_t ld_dw;
 
@@ -354,8 +444,8 @@ __device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int pie
     int tp, tq;
     product_tile(at, np, nq, tp, tq);
     const int p0 = b.first(piece) + tp * Tile::kP, q0 = tq * Tile::kQ;
-    // what the tile's rows take: the maximum, weight / (T s), weight / T (both in units) and the
-    // target within the tile
+    // what the tile's rows take: the maximum, weight / (T s), weight / T and the target within the
+    // tile
     __shared__ float4 rows_of[Tile::kQ];
     Tile t;
     logits(t, lds, b.w, b.x, p0, count, q0, [&] {
@@ -365,7 +455,7 @@ __device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int pie
                 const int row = b.x.row[q0 + q];
                 const int target = b.a.targets[row];
                 const float2 st = b.stats[row];
-                float scale = (b.a.weight ? b.a.weight[row] : 1.0f) * b.heat.inv / *b.x.unit;
+                float scale = (b.a.weight ? b.a.weight[row] : 1.0f) * b.heat.inv;
                 if (target >= b.w.vocab)
                     scale = NAN;
                 v = make_float4(base_of(st.x), st.y == 0.0f ? 0.0f : scale / st.y, scale,
@@ -382,6 +472,8 @@ __device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int pie
         const float base = row.x, inv = row.y, scale = row.z;
         const int target = __float_as_int(row.w);
         const bool near = __any((unsigned)target < (unsigned)Tile::kP);
+        bool found = false;
+        float rest = 0.0f;
 #pragma unroll
         for (int i = 0; i < Tile::NP; ++i) {
             float d[4];
@@ -391,7 +483,11 @@ __device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int pie
             if (near) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    d[r] -= t.p_of(i) + r == target ? scale : 0.0f;
+                    if (t.p_of(i) + r == target) {
+                        d[r] -= scale;
+                        rest = rounding_left(d[r]);
+                        found = true;
+                    }
             }
             if (!whole || q0 + Tile::kQ > count) {
 #pragma unroll
@@ -400,6 +496,8 @@ __device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int pie
             }
             t.put(lds, i, j, (gv2u){pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])});
         }
+        if (found)
+            b.left[q0 + t.q_of(j)] = make_int4(p0 + target, __float_as_int(rest), 0, 0);
     }
     u16 *to = b.dz + (int64_t)q0 * b.ld + tp * Tile::kP;
     t.template flush<false>(lds, to, b.ld, Tile::kQ, Tile::kP);
@@ -452,6 +550,133 @@ __device__ __forceinline__ void dx_part(uint8_t *lds, const Backward &b, int pie
         }
 }
 
+// What the rounding of dz left at the targets, times x, into the sums of a tile of dw: the rows with
+// their target in the tile are a product of their own, up to 64 of them a step, behind the tile's.
+// Their x is fetched from where it lies; the other operand is zero but for one value a row (in bf16: off
+// by 2^-9 of what is 2^-9 of dz), which is put into the LDS and taken out again.
+//
+// Most tiles have at most 32 such rows.  Those are fetched to a place of their own with the tile's
+// own first steps (dw of 1024 rows under 16000 x 512 26.8 us, 30.8 with all of them fetched behind the
+// tile's product, 24.5 without any), except where there is one step only and the workgroups share a CU.
+// Many rows to an entry cost the most: dw of 8192 rows under 1000 x 4096 92 us, 76 without.
+template <class Tile> struct Rests {
+    using SideP = typename Tile::SideP;
+    using SideQ = typename Tile::SideQ;
+    static constexpr bool kEarly = Tile::kSlots > 1;
+    static constexpr int kOther = Tile::kSlots * SideP::kBytes;  // the other operand's place
+    struct Shared {
+        uint8_t early[kEarly ? SideP::kBytes / 2 : 16];  // x of 32 rows
+        int4 left[2][64];
+    };
+    const Backward &b;
+    Shared &shared;
+    int from, end;    // the tile's rows in the list, from the next step's
+    int fetched = 0;  // early
+
+    __device__ __forceinline__ Rests(const Backward &b_, Shared &shared_, int tile)
+        : b(b_), shared(shared_), from(__builtin_amdgcn_readfirstlane(b.starts[tile])),
+          end(__builtin_amdgcn_readfirstlane(b.starts[tile + 1]))
+    {
+    }
+    // Fetches the next rows, up to `most`: COPIES copies of x a wave to `to`, its first one's place, and
+    // what is left of them (all waves the same) to a slot; returns how many.
+    template <int COPIES>
+    __device__ __forceinline__ int fetch(const Tile &t, int most, int slot, uint32_t to, int p0)
+    {
+        const int all = min(end - from, most);
+        if (all <= 0)
+            return 0;
+        const int row = b.by_target[from + min(t.lane, all - 1)];
+        from += all;
+        const uint8_t *zeros = reinterpret_cast<const uint8_t *>(kZeros);
+        copy16(t.lane < all ? reinterpret_cast<const uint8_t *>(b.left + row) : zeros,
+               __builtin_amdgcn_readfirstlane(lds_address(shared.left[slot])));
+#pragma unroll
+        for (int n = 0; n < COPIES; ++n) {
+            const int cc = t.wave + n * Tile::kWaves;
+            const int k = cc * (512 / Tile::kP) + t.lane / (Tile::kP / 8);
+            const uint8_t *at = reinterpret_cast<const uint8_t *>(
+                b.x.x + (int64_t)__shfl(row, k) * b.x.ld + p0);
+            copy16(k < all ? at + SideP::offset(cc, t.lane, 0, b.x.ld - p0) : zeros,
+                   to + n * (Tile::kWaves * 1024));
+        }
+        return all;
+    }
+    // while the tile's first steps are fetched; p0: its first hidden value
+    __device__ __forceinline__ void early(const Tile &t, int p0)
+    {
+        if constexpr (kEarly)
+            fetched = fetch<Tile::kPerP / 2>(
+                t, 32, 0,
+                __builtin_amdgcn_readfirstlane(lds_address(shared.early) + t.wave * 1024), p0);
+    }
+    // behind the tile's product; v0: its first entry of the vocabulary
+    __device__ __forceinline__ void add(Tile &t, uint8_t *lds, int v0, int p0)
+    {
+        int now = kEarly ? fetched : fetch<Tile::kPerP>(t, 64, 0, t.at_p, p0);
+        if (now <= 0)
+            return;
+        for (int i = threadIdx.x * 16; i < SideQ::kBytes; i += Tile::kThreads * 16)
+            *reinterpret_cast<gv4u *>(lds + kOther + i) = (gv4u){0u, 0u, 0u, 0u};
+        uint16_t *value = nullptr;
+        int slot = 0;
+        uint32_t at = kEarly ? lds_address(shared.early) : lds_address(lds);
+        while (now > 0) {
+            // the step's rows have landed, and everyone is done with those before
+            Tile::template wait<0>();
+            barrier_no_fence();
+            const int4 left = shared.left[slot][t.lane];
+            // (within the tile, whatever became of the targets in the meantime)
+            const int column = t.lane < now && (unsigned)(left.x - v0) < (unsigned)Tile::kQ ? left.x - v0 : -1;
+            if (t.wave == 0) {
+                if (value)
+                    *value = 0;
+                value = column < 0 ? nullptr
+                                   : reinterpret_cast<uint16_t *>(lds + kOther + SideQ::place(t.lane, column));
+                if (value)
+                    *value = __builtin_bit_cast(uint16_t, (__bf16)__int_as_float(left.y));
+            }
+            int then = 0;
+            if (kEarly)
+                then = fetch<Tile::kPerP>(t, 64, slot ^ 1, t.at_p + (slot ^ 1) * SideP::kBytes, p0);
+            Tile::template wait<63>();
+            barrier_no_fence();
+            t.read_p.start(at, t.wp, t.lane);
+            t.read_q.start(lds_address(lds) + kOther, t.wq, t.lane);
+            uint64_t on[Tile::NQ];
+#pragma unroll
+            for (int j = 0; j < Tile::NQ; ++j)
+                on[j] = __ballot(column >> 4 == t.wq + Tile::WQ * j);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (now <= 32 * h)
+                    break;
+                v8bf x[Tile::NP];
+#pragma unroll
+                for (int i = 0; i < Tile::NP; ++i)
+                    x[i] = t.read_p.read(i, h);
+#pragma unroll
+                for (int j = 0; j < Tile::NQ; ++j)
+                    if ((uint32_t)(on[j] >> (32 * h))) {
+                        const v8bf rests = t.read_q.read(j, h);
+#pragma unroll
+                        for (int i = 0; i < Tile::NP; ++i)
+                            t.acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], rests, t.acc[i][j], 0, 0, 0);
+                    }
+            }
+            if constexpr (kEarly) {
+                now = then;
+                slot ^= 1;
+                at = lds_address(lds) + slot * SideP::kBytes;
+            } else {
+                barrier_no_fence();
+                now = fetch<Tile::kPerP>(t, 64, 0, t.at_p, p0);
+            }
+        }
+        barrier_no_fence();
+    }
+};
+
 // Tile `at` of dw = dz^T x of the piece's vocabulary.
 template <class Tile>
 __device__ __forceinline__ void dw_part(uint8_t *lds, const Backward &b, int piece, int at)
@@ -464,18 +689,24 @@ __device__ __forceinline__ void dw_part(uint8_t *lds, const Backward &b, int pie
     int tp, tq;
     product_tile(at, np, nq, tp, tq);
     const int p0 = tp * Tile::kP, q0 = tq * Tile::kQ;
+    __shared__ __align__(16) typename Rests<Tile>::Shared shared;
+    const int v0 = b.first(piece) + q0;
+    const int count = *b.x.count;
+    Rests<Tile> rests(b, shared, v0 / Tile::kQ);  // on its way with the count
     Tile t;
     t.start(lds, b.x.ld, b.x.ld - p0, b.ld, b.width - q0, kStepK);
     const uint8_t *p = reinterpret_cast<const uint8_t *>(b.x.x + p0);
     const uint8_t *q = reinterpret_cast<const uint8_t *>(b.dz + q0);
-    t.run((*b.x.count + kStepK - 1) / kStepK, p, kStepK * 2 * b.x.ld, q, kStepK * 2 * b.ld, 0,
-          [] {});
-    const float unit = *b.x.unit;
+    t.run((count + kStepK - 1) / kStepK, p, kStepK * 2 * b.x.ld, q, kStepK * 2 * b.ld, 0,
+          [&] { rests.early(t, p0); });
+    t.place();  // nothing more is kept over the product, whose tiles fill the registers
+    rests.add(t, lds, v0, p0);
+    t.place();
 #pragma unroll
     for (int j = 0; j < Tile::NQ; ++j)
 #pragma unroll
         for (int i = 0; i < Tile::NP; ++i) {
-            const v4f v = t.acc[i][j] * unit;
+            const v4f v = t.acc[i][j];
             t.put(lds, i, j, (gv2u){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
         }
     t.template flush<true>(lds, b.dw + (int64_t)(b.first(piece) + q0) * b.ld_dw + p0, b.ld_dw,
@@ -510,21 +741,28 @@ __global__ __launch_bounds__(256) void k_ce_dx_rows(Backward b, int p, int q, bf
     const int count = *b.x.count;
     const int slabs = slabs_of((hidden + p - 1) / p * ((count + q - 1) / q), b.fill, b.room);
     const int64_t slab = (int64_t)count * hidden;
-    const float unit = *b.x.unit;
     for (int64_t i = blockIdx.x; i < b.a.rows * wide; i += gridDim.x) {
         const int64_t r = i / wide;
         const int c = (int)(i % wide) * 1024 + threadIdx.x * 4;
         if (c >= hidden)
             continue;
-        const int at = b.x.place[r];
+        const int at = b.x.place[r], target = b.a.targets[r];
         v4f v = {0.f, 0.f, 0.f, 0.f};
         if (at >= 0) {
+            const bool here = target < b.w.vocab;
+            const gv2u raw = *(const MXQ_GLOBAL gv2u *)(b.w.w + (int64_t)(here ? target : 0) * b.w.ld + c);
+            const float rest = here ? __int_as_float(b.left[at].y) : 0.0f;
             const float *from = b.sums + (int64_t)at * hidden + c;
 #pragma unroll 8
             for (int s = 0; s < slabs; ++s)
                 v += *reinterpret_cast<const v4f *>(from + s * slab);
+            float w[4];
+            unpack(raw, w, (bf16_t *)nullptr);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] += rest_of(rest, w[k]);
         }
-        const float f[4] = {v[0] * unit, v[1] * unit, v[2] * unit, v[3] * unit};
+        const float f[4] = {v[0], v[1], v[2], v[3]};
         store_vec(dx + r * ld + c, f);
     }
 }
@@ -559,7 +797,6 @@ CePacked take_packed(Carve &c, int64_t rows, int64_t hidden)
     CePacked x;
     x.all = -1;
     x.count = c.take<int>(1);
-    x.unit = c.take<float>(1);
     x.place = c.take<int>(rows);
     x.row = c.take<int>(rows);
     x.at_target = c.take<float>(rows);
@@ -681,6 +918,7 @@ struct BackwardPlan {
     Backward b;  // without the caller's pointers
     int64_t pieces;
     int64_t dx_groups, dx_p, dx_q;  // workgroups of the products for dx, and their tile
+    int dw_q;                       // entries of the vocabulary of a tile of dw
     size_t bytes;
 };
 // a piece's width is a multiple of it, and so is how many rows dz has: of every tile's
@@ -700,6 +938,10 @@ BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws
     b.width = (int)width;
     b.ld = (int)pitch(width);
     b.dz = c.take<u16>(padded * b.ld);
+    with_dw(rows, hidden, width, [&](auto t) { f.dw_q = decltype(t)::Tile::kQ; });
+    b.by_target = c.take<int>(rows);
+    b.starts = c.take<int>(tiles_of(vocab, f.dw_q) + 1);
+    b.left = c.take<int4>(rows);
     with_dx(rows, hidden, width, vocab, [&](auto t) {
         using Tile = typename decltype(t)::Tile;
         const int64_t np = tiles_of(hidden, Tile::kP), tiles = np * tiles_of(rows, Tile::kQ);
@@ -739,15 +981,15 @@ mxq_status check(const void *x, int64_t ld_x, const void *w, int64_t ld_w, int64
     return MXQ_OK;
 }
 
-void launch_pack(const CeRows &a, const void *x, int64_t ld, int64_t hidden, float inv_t,
-                 const CePacked &to, bool zeros, hipStream_t s)
+void launch_pack(const CeRows &a, const void *x, int64_t ld, int64_t hidden, const CePacked &to,
+                 bool zeros, const CeTargets &lists, hipStream_t s)
 {
     // about 1024 workgroups: more would read the rows in front of their own more often
     const int64_t per = a.rows > 1024 ? tiles_of(a.rows, 1024) : 1;
     const int groups = (int)(a.rows > 0 ? tiles_of(a.rows, per) : 1);
-    hipLaunchKernelGGL(k_ce_pack, dim3((unsigned)(groups + (zeros ? kStepK - 1 : 0))),
+    hipLaunchKernelGGL(k_ce_pack, dim3((unsigned)(groups + (zeros ? kStepK - 1 + lists.tiles : 0))),
                        dim3(kPackThreads), 0, s, a, per, groups, static_cast<const bf16_t *>(x), ld,
-                       (int)hidden, inv_t, to);
+                       (int)hidden, to, lists);
 }
 
 }  // namespace
@@ -800,7 +1042,7 @@ extern "C" mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const v
             f.x.x = const_cast<u16 *>(static_cast<const u16 *>(x));
             f.x.ld = (int)ld_x;
         } else {
-            launch_pack(a, x, ld_x, hidden, heat.inv, f.x, false, s);
+            launch_pack(a, x, ld_x, hidden, f.x, false, {}, s);
         }
         hipLaunchKernelGGL(k_ce_stats<Tile>, dim3((unsigned)groups), dim3(Tile::kThreads), 0, s, cw,
                            a, f.x, heat, f.part, f.stride);
@@ -851,7 +1093,9 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
     b.stats = reinterpret_cast<const float2 *>(stats);
     b.dw = static_cast<u16 *>(dw);
     b.ld_dw = ld_dw;
-    launch_pack(b.a, x, ld_x, hidden, b.heat.inv, b.x, true, s);
+    const CeTargets lists = {dw ? (int)tiles_of(vocab, f.dw_q) : 0, __builtin_ctz(f.dw_q), (int)vocab, b.stats,
+                             b.by_target, b.starts};
+    launch_pack(b.a, x, ld_x, hidden, b.x, true, lists, s);
     const auto have = [&](int64_t piece) {
         return vocab - piece * b.width < b.width ? vocab - piece * b.width : (int64_t)b.width;
     };

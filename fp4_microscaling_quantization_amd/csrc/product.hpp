@@ -75,6 +75,13 @@ template <int ROWS, bool ALONG> struct Side {
         }
     }
 
+    // where value k of row `row` of an operand across k lies in a step's tile, in bytes
+    static __device__ __forceinline__ int place(int k, int row)
+    {
+        static_assert(!ALONG, "across k");
+        return k * (ROWS * 2) + ((row >> 3) ^ (2 * (k & 7))) * 16 + (row & 7) * 2;
+    }
+
     // Where a wave's fragments lie: wave w of W takes fragments (of 16 rows) w, w + W, ...
     // A lane keeps kBases addresses; fragment i and the half are constants from there.
     template <int W> struct Reader {
@@ -147,7 +154,7 @@ template <int WP_, int WQ_, int NP_, int NQ_, int SLOTS, bool P_ALONG, bool Q_AL
 struct Product {
     static constexpr int WP = WP_, WQ = WQ_, NP = NP_, NQ = NQ_;
     static constexpr int kP = 16 * WP * NP, kQ = 16 * WQ * NQ, kWaves = WP * WQ;
-    static constexpr int kThreads = 64 * kWaves;
+    static constexpr int kThreads = 64 * kWaves, kSlots = SLOTS;
     using SideP = Side<kP, P_ALONG>;
     using SideQ = Side<kQ, Q_ALONG>;
     static constexpr int kLds = SLOTS * (SideP::kBytes + SideQ::kBytes);
@@ -191,8 +198,10 @@ struct Product {
 
     __device__ __forceinline__ void place()
     {
-        lane = threadIdx.x & 63;
-        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        int thread = threadIdx.x;
+        asm volatile("" : "+v"(thread));
+        lane = thread & 63;
+        wave = __builtin_amdgcn_readfirstlane(thread >> 6);
         wp = wave % WP;
         wq = wave / WP;
     }

@@ -470,8 +470,9 @@ mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t ro
  *    multiple of 32.  w and dw are 16-byte aligned, their leading dimensions
  *    multiples of 8 and at most 2^22; x and dx stand at any element.  hidden is
  *    at most 2^16, vocab 2^24, rows 2^22, rows x vocab 2^37.
- *  - Products of bf16 values are summed in fp32; dz is rounded to bf16 once,
- *    dx and dw where they are stored.
+ *  - Products of bf16 values are summed in fp32; dz is rounded to bf16, dx and dw
+ *    where they are stored.  What the rounding leaves of dz at a row's target, mostly
+ *    its largest entry, is added to both sums (to dw in bf16 of its own).
  *  - A row with a target < 0 or a weight of 0 does not count: loss 0, stats
  *    (0, 1), dx 0, nothing in dw, whatever else it holds; and it costs nothing.  A
  *    target >= vocab makes its row's loss and dx NaN, and dw with them.  Rows that
