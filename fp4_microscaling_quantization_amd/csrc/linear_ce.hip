@@ -456,10 +456,12 @@ __device__ __forceinline__ void dlogits(uint8_t *lds, const Backward &b, int pie
                 const int target = b.a.targets[row];
                 const float2 st = b.stats[row];
                 float scale = (b.a.weight ? b.a.weight[row] : 1.0f) * b.heat.inv;
-                if (target >= b.w.vocab)
+                const bool foreign = target >= b.w.vocab;
+                if (foreign)
                     scale = NAN;
-                v = make_float4(base_of(st.x), st.y == 0.0f ? 0.0f : scale / st.y, scale,
-                                __int_as_float(target - p0));
+                // (q is 0 in a row with every logit masked, NaN in one with a foreign target)
+                v = make_float4(base_of(st.x), st.y == 0.0f && !foreign ? 0.0f : scale / st.y,
+                                scale, __int_as_float(target - p0));
             }
             rows_of[q] = v;
         }
