@@ -779,6 +779,24 @@ def _dense(t) -> bool:
     return True
 
 
+def _refuse_overlaps(spans):
+    """Refuses an output that shares memory with another tensor of the list, or with a part of its own gradient.
+    spans: (first byte, end, whether it is written, place in the list)."""
+    def name(write, i):
+        return f"{'output' if write else 'gradient'} {i}"
+    read = written = (0, 0, False, 0)    # of the spans so far, those that end last
+    for span in sorted(spans):
+        at, end, write, i = span
+        other = read if write and read[1] > written[1] else written
+        if at < other[1]:
+            one, two = (name(write, i), name(*other[2:]))[::1 if write else -1]
+            raise ValueError(f"{one}: in the same memory as {two}")
+        if write:
+            written = max(written, span, key=lambda s: s[1])
+        elif end > read[1]:
+            read = span
+
+
 def _grad_list(grads, out=None, write=True):
     """The mxq_grad array of a list of tensors (written in place, or to the list `out`), and what it points into."""
     grads = list(grads)
@@ -787,19 +805,26 @@ def _grad_list(grads, out=None, write=True):
         raise ValueError("no gradients: the device is theirs")
     if len(out) != len(grads):
         raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
-    first, seen = grads[0], set()
+    device, spans = grads[0].device, []
     arr = (Grad * len(grads))()
+
+    def seen(name, i, t):
+        if t.device != device or not _dense(t):
+            raise ValueError(f"{name} {i}: a dense tensor on {device} expected, not strides {t.stride()} on {t.device}")
+        return t.data_ptr(), _dtype(t)
     for i, (g, o) in enumerate(zip(grads, out)):
-        for name, t in (("gradient", g), ("output", o)):
-            if t.device != first.device or not _dense(t):
-                raise ValueError(f"{name} {i}: a dense tensor on {first.device} expected, not strides {t.stride()} on {t.device}")
-        if o is not g and (o.shape != g.shape or o.stride() != g.stride()):
-            raise ValueError(f"output {i}: shape {tuple(o.shape)} strides {o.stride()}, not {tuple(g.shape)} {g.stride()}")
+        at, code = to, to_code = seen("gradient", i, g)
         n = g.numel()
-        if write and n and o.data_ptr() in seen:
-            raise ValueError(f"output {i}: the same memory as another one")
-        seen.add(o.data_ptr())
-        arr[i] = Grad(g.data_ptr(), o.data_ptr(), n, _dtype(g), _dtype(o))
+        if o is not g:
+            to, to_code = seen("output", i, o)
+            if o.shape != g.shape or o.stride() != g.stride():
+                raise ValueError(f"output {i}: shape {tuple(o.shape)} strides {o.stride()}, not {tuple(g.shape)} {g.stride()}")
+        arr[i] = Grad(at, to, n, code, to_code)
+        if write and n:
+            spans.append((to, to + n * (4 if to_code == OUT_F32 else 2), True, i))
+            if at != to:
+                spans.append((at, at + n * (4 if code == OUT_F32 else 2), False, i))
+    _refuse_overlaps(spans)
     return arr, (grads, out)
 
 
@@ -808,7 +833,10 @@ def prepare_grad_norm(grads):
     stream (or `stream`) again and returns the same (norm, sum_sq) tensors.  It
     holds the gradients and a workspace, made on the stream that is current here;
     calls of it that overlap race."""
-    arr, keep = _grad_list(grads, write=False)
+    return _prepared_norm(*_grad_list(grads, write=False))
+
+
+def _prepared_norm(arr, keep):
     first = keep[0][0]
     torch, _ = _enter(first, None)
     size = lib().mxq_grad_norm_workspace_size(arr, len(arr))
@@ -831,7 +859,7 @@ def prepare_clip_grad_norm(grads, max_norm, *, eps, out=None):
     current here; calls of it that overlap race."""
     arr, keep = _grad_list(grads, out)
     first = keep[0][0]
-    measure = prepare_grad_norm(keep[0])
+    measure = _prepared_norm(arr, keep)
     fn = lib().mxq_grad_clip
 
     def call(stream=None):
@@ -845,7 +873,10 @@ def prepare_clip_grad_norm(grads, max_norm, *, eps, out=None):
 def grad_norm(grads, stream=None):
     """mxq_grad_norm: (norm, sum_sq) over a list of tensors, fp32 and fp64 scalars."""
     arr, keep = _grad_list(grads, write=False)
-    first = keep[0][0]
+    return _norm(arr, keep[0][0], stream)
+
+
+def _norm(arr, first, stream):
     torch, handle = _enter(first, stream)
     size = lib().mxq_grad_norm_workspace_size(arr, len(arr))
     ws = _new(first, (max(size, 8),), torch.uint8, stream)
@@ -856,9 +887,13 @@ def grad_norm(grads, stream=None):
 
 def grad_clip(grads, sum_sq, max_norm, *, eps, out=None, stream=None):
     """mxq_grad_clip: the gradients scaled to max_norm by a sum of squares (fp64), in
-    place or into `out`, a list of tensors of the same shapes."""
+    place or into `out`, a list of tensors of the same shapes, which may share memory
+    with no other of them."""
     arr, keep = _grad_list(grads, out)
-    first = keep[0][0]
+    _clip(arr, keep[0][0], sum_sq, max_norm, eps, stream)
+
+
+def _clip(arr, first, sum_sq, max_norm, eps, stream):
     torch, handle = _enter(first, stream)
     _check("mxq_grad_clip", lib().mxq_grad_clip(
         arr, len(arr), _vector("sum_sq", sum_sq, (), first, torch.float64), max_norm, eps, handle))
@@ -866,7 +901,7 @@ def grad_clip(grads, sum_sq, max_norm, *, eps, out=None, stream=None):
 
 def clip_grad_norm(grads, max_norm, *, eps, out=None, stream=None):
     """grad_norm, then grad_clip by it; returns the norm."""
-    grads = list(grads)
-    norm, sum_sq = grad_norm(grads, stream)
-    grad_clip(grads, sum_sq, max_norm, eps=eps, out=out, stream=stream)
+    arr, keep = _grad_list(grads, out)
+    norm, sum_sq = _norm(arr, keep[0][0], stream)
+    _clip(arr, keep[0][0], sum_sq, max_norm, eps, stream)
     return norm

@@ -513,8 +513,9 @@ size_t mxq_linear_ce_backward_workspace_size(int64_t rows, int64_t hidden, int64
  *  - A norm that is infinite gives c = 0, one that is NaN c = NaN, in IEEE
  *    arithmetic (infinities become NaN, and everything does).
  *  - Empty tensors and empty lists serve (norm 0); a list has at most 2^38
- *    elements.  An out may overlap no other tensor's g or out.  max_norm and
- *    eps are finite and >= 0; where max_norm, norm and eps are all 0, c is NaN.
+ *    elements.  An out may overlap no other tensor's g or out, nor a part of its
+ *    own g (these calls do not look for it).  max_norm and eps are finite and
+ *    >= 0; where max_norm, norm and eps are all 0, c is NaN.
  *  - mxq_grad_norm only reads g, n and dtype.
  * workspace: mxq_grad_norm_workspace_size(grads, count) bytes, 8-byte aligned (0
  * for empty lists and those that are refused). */
