@@ -779,6 +779,12 @@ def _dense(t) -> bool:
     return True
 
 
+def _same_order(a, b) -> bool:
+    """Whether two dense tensors of one shape have their elements in the same order: strides count where
+    there is a step to take."""
+    return a.numel() == 0 or all(s == t for s, t, size in zip(a.stride(), b.stride(), a.shape) if size > 1)
+
+
 def _refuse_overlaps(spans):
     """Refuses an output that shares memory with another tensor of the list, or with a part of its own gradient.
     spans: (first byte, end, whether it is written, place in the list)."""
@@ -817,7 +823,7 @@ def _grad_list(grads, out=None, write=True):
         n = g.numel()
         if o is not g:
             to, to_code = seen("output", i, o)
-            if o.shape != g.shape or o.stride() != g.stride():
+            if o.shape != g.shape or (o.stride() != g.stride() and not _same_order(o, g)):
                 raise ValueError(f"output {i}: shape {tuple(o.shape)} strides {o.stride()}, not {tuple(g.shape)} {g.stride()}")
         arr[i] = Grad(at, to, n, code, to_code)
         if write and n:
