@@ -7,7 +7,8 @@ instructions disabled.
 
 Beside it stands libmxq_loop.so, for the tests: the same library with launches
 over rows of at most LOOP_GRID workgroups, so that few rows make every
-workgroup take several in turn, and with pieces of the vocabulary of one tile.
+workgroup take several in turn, with pieces of the vocabulary of one tile, and
+with a function that says which kernels a size takes.
 """
 import glob
 import os
@@ -59,7 +60,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
         name = os.path.basename(src)
         objs.append(compile_to(src, os.path.join(objdir, name + ".o"), []))
         loop_objs.append(compile_to(src, os.path.join(objdir, name + ".loop.o"),
-                                    [f"-DMXQ_ROW_GRID={LOOP_GRID}", "-DMXQ_PIECE_LOGITS=1"]) if name in LOOP_SOURCES else objs[-1])
+                                    [f"-DMXQ_ROW_GRID={LOOP_GRID}", "-DMXQ_PIECE_LOGITS=1", "-DMXQ_TESTS"]) if name in LOOP_SOURCES else objs[-1])
     for p in procs:
         _wait(p)
     link(objs, LIB)

@@ -426,7 +426,7 @@ struct Backward {
 
 // The products for dx are split over stretches of a piece's vocabulary until they fill the
 // chip; each stretch has its own slab of sums.  How many rows count is only known here.
-__device__ __forceinline__ int slabs_of(int tiles, int fill, int room)
+__host__ __device__ __forceinline__ int slabs_of(int tiles, int fill, int room)
 {
     return tiles >= fill ? 1 : max(1, min(fill / max(1, tiles), room));
 }
@@ -925,7 +925,8 @@ struct BackwardPlan {
 };
 // a piece's width is a multiple of it, and so is how many rows dz has: of every tile's
 constexpr int kWidthStep = 256, kRowStep = 256;
-BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws)
+BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws,
+                           int64_t piece_logits = kPieceLogits)
 {
     BackwardPlan f;
     Carve c = {static_cast<uint8_t *>(ws)};
@@ -933,7 +934,7 @@ BackwardPlan backward_plan(int64_t rows, int64_t hidden, int64_t vocab, void *ws
     b.x = take_packed(c, rows, hidden);
     const int64_t padded = up(rows > 0 ? rows : 1, kRowStep);
     const int64_t most = up(vocab, kWidthStep);
-    int64_t width = kPieceLogits / padded / kWidthStep * kWidthStep;
+    int64_t width = piece_logits / padded / kWidthStep * kWidthStep;
     width = width < kWidthStep ? kWidthStep : width < most ? width : most;
     width = up(tiles_of(vocab, tiles_of(vocab, width)), kWidthStep);
     f.pieces = tiles_of(vocab, width);
@@ -1132,3 +1133,30 @@ extern "C" mxq_status mxq_linear_ce_backward(const void *x, int64_t ld_x, const 
                            0, s, b, (int)f.dx_p, (int)f.dx_q, static_cast<bf16_t *>(dx), ld_dx);
     return launched();
 }
+
+#ifdef MXQ_TESTS
+// For the tests, in their build of the library alone: the kernels that calls of these sizes take, with
+// pieces of up to piece_logits logits.  tiles: [forward logits, backward logits, dx, dw][their p, q, steps
+// in LDS, whether a last step may be cut]; plan: pieces, their width, most slabs of dx.
+extern "C" void mxq_linear_ce_kernels(int64_t rows, int64_t hidden, int64_t vocab,
+                                      int64_t piece_logits, int32_t *tiles, int32_t *plan)
+{
+    const BackwardPlan f = backward_plan(rows, hidden, vocab, nullptr, piece_logits);
+    const auto put = [&](int i) {
+        return [&tiles, i](auto t) {
+            using Tile = typename decltype(t)::Tile;
+            const int32_t v[4] = {Tile::kP, Tile::kQ, Tile::kSlots, Tile::kCut};
+            for (int k = 0; k < 4; ++k)
+                tiles[4 * i + k] = v[k];
+        };
+    };
+    with_logits<true>(rows, hidden, vocab, put(0));
+    with_logits<false>(rows, hidden, f.b.width, put(1));
+    with_dx(rows, hidden, f.b.width, vocab, put(2));
+    with_dw(rows, hidden, f.b.width, put(3));
+    const int64_t of_dx = tiles_of(hidden, f.dx_p) * tiles_of(rows, f.dx_q);
+    plan[0] = (int32_t)f.pieces;
+    plan[1] = f.b.width;
+    plan[2] = slabs_of((int)of_dx, f.b.fill, f.b.room);
+}
+#endif

@@ -155,6 +155,7 @@ struct Product {
     static constexpr int WP = WP_, WQ = WQ_, NP = NP_, NQ = NQ_;
     static constexpr int kP = 16 * WP * NP, kQ = 16 * WQ * NQ, kWaves = WP * WQ;
     static constexpr int kThreads = 64 * kWaves, kSlots = SLOTS;
+    static constexpr bool kCut = P_CUT;
     using SideP = Side<kP, P_ALONG>;
     using SideQ = Side<kQ, Q_ALONG>;
     static constexpr int kLds = SLOTS * (SideP::kBytes + SideQ::kBytes);
