@@ -726,6 +726,40 @@ def _bf16(name, t, shape, like):
     return p, ld
 
 
+def _rows_of(t):
+    """(address, bytes between rows, bytes of a row, rows) of a matrix whose rows are contiguous, or a packed vector."""
+    size = t.element_size()
+    if t.dim() == 2 and t.shape[0] > 1 and not t.is_contiguous():
+        return t.data_ptr(), t.stride(0) * size, t.shape[1] * size, t.shape[0]
+    return t.data_ptr(), t.numel() * size, t.numel() * size, 1
+
+
+def _share(a, b) -> bool:
+    """Whether two such tensors have a byte in common; interleaved columns of one buffer have none."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (p, ld_p, wide_p, rows_p), (q, ld_q, wide_q, rows_q) = sorted((_rows_of(a), _rows_of(b)), key=lambda r: r[3])
+    if p + (rows_p - 1) * ld_p + wide_p <= q or q + (rows_q - 1) * ld_q + wide_q <= p:
+        return False
+    if ld_p == ld_q:
+        between, (first, second) = abs(q - p) % ld_p, (wide_p, wide_q) if p <= q else (wide_q, wide_p)
+        return between < first or between + second > ld_p
+    for at in range(p, p + rows_p * ld_p, ld_p):
+        # the first of the other's rows that ends behind this one's start
+        row = max(0, (at - q - wide_q) // ld_q + 1)
+        if row < rows_q and q + row * ld_q < at + wide_p:
+            return True
+    return False
+
+
+def _refuse_shared(**tensors):
+    """Refuses an output (dx, dw) that shares memory with another tensor of the call."""
+    for name in ("dx", "dw"):
+        for other, t in tensors.items():
+            if other != name and tensors[name] is not None and t is not None and _share(tensors[name], t):
+                raise ValueError(f"{name}: in the same memory as {other}")
+
+
 def linear_ce_forward(x, w, targets, weight=None, *, temperature=1, stream=None):
     """mxq_linear_ce_forward: (loss, stats) of the output layer with weight w
     [vocab, hidden] on the hidden states x [rows, hidden]."""
@@ -745,7 +779,7 @@ def linear_ce_forward(x, w, targets, weight=None, *, temperature=1, stream=None)
 
 def linear_ce_backward(x, w, targets, stats, weight=None, *, temperature=1, dx=True, dw=True, stream=None):
     """mxq_linear_ce_backward: (dx, dw), new tensors for True, None for False; a
-    tensor takes the gradient itself."""
+    tensor takes the gradient itself, and shares memory with no other one."""
     torch, handle = _enter(x, stream)
     (rows, hidden), vocab = x.shape, w.shape[0]
     xp, ldx = _bf16("x", x, (rows, hidden), x)
@@ -756,8 +790,11 @@ def linear_ce_backward(x, w, targets, stats, weight=None, *, temperature=1, dx=T
             return None, None, 0
         t = _new(x, shape, torch.bfloat16, stream) if given is True else given
         return (t, *_bf16(name, t, shape, x))
+    own = any(torch.is_tensor(t) for t in (dx, dw))
     dx, dxp, lddx = gradient("dx", dx, (rows, hidden))
     dw, dwp, lddw = gradient("dw", dw, (vocab, hidden))
+    if own:
+        _refuse_shared(dx=dx, dw=dw, x=x, w=w, targets=targets, stats=stats, weight=weight)
     size = lib().mxq_linear_ce_backward_workspace_size(rows, hidden, vocab)
     ws = _new(x, (size,), torch.uint8, stream) if size else None
     _check("mxq_linear_ce_backward", lib().mxq_linear_ce_backward(
