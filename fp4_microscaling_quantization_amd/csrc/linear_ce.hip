@@ -828,11 +828,15 @@ constexpr int64_t kPieceLogits = MXQ_PIECE_LOGITS;
 // 4096 x 128256 in the forward pass 205 us without the hint, 182 with it).
 template <bool ONCE, bool CUT, class F> void with_logits_of(int64_t rows, int64_t vocab, F f)
 {
-    // Forward passes: 4 rows under 8000 x 4096 (125 tiles) Slim 21 us, Few 34; 16 under 32003 x 4096
-    // (501) 56 and 50.  100 rows under 8000 x 4096 (250) Small 36 us, Deep 42; under 16000 (500) 64
-    // and 49.  200 under 8000 x 4096 (500) Small 58, Half 68; 300 (625) 77 and 64.  100 under
-    // 32000 x 4096 (250) Deep 64 us, Twin 78; under 128256 222 and 203.  200 under 32000 x 4096
-    // (125) Half 79 us, Many 126; 400 (250) 153 and 135.
+    // Forward passes, with weights that no cache holds yet: 4 rows under 8000 x 4096 (125 tiles) Slim
+    // 21 us, Few 34; 16 under 32003 x 4096 (501) 56 and 50.  100 rows under 8000 x 4096 (250) Small
+    // 36 us, Deep 42; under 16000 (500) 64 and 49.  200 under 8000 x 4096 (500) Small 58, Half 68;
+    // 300 (625) 77 and 64.  100 under 32000 x 4096 (250) Deep 64 us, Twin 78; under 128256 222 and 203.
+    // 200 under 32000 x 4096 (125) Half 79 us, Many 126; 400 (250) 153 and 135.
+    // Deep and Twin above 128 rows: 200 under 8000 x 4096 54 and 70 (Small 57), under 16000 x 4096 62
+    // and 76 (Half 71), under 32000 x 4096 114 and 114, under 32000 x 1024 38 and 36 (Half 30); 400
+    // under 8000 x 1024 24 and 29 (Half 27), under 16000 x 4096 115 and 115 (Half 76), under 32000 x
+    // 1024 68 and 63 (Many 43).  Deep's few better sizes, by 13% at most, lie on both sides of these rules.
     const int64_t small = tiles_of(vocab, 64) * tiles_of(rows, 64);
     if (rows <= 32 && small <= kCus)
         f(Tag<Slim<true, true, CUT, ONCE>>{});
@@ -885,7 +889,12 @@ template <class F> void with_dx(int64_t rows, int64_t hidden, int64_t width, int
 // for dw
 template <class F> void with_dw(int64_t rows, int64_t hidden, int64_t vocab, F f)
 {
-    // 1024 rows under 8000 x 512 (64 tiles) forward and backward Deep 70 us, Many 83
+    // 1024 rows under 8000 x 512 (64 tiles) forward and backward Deep 70 us, Many 83.  Passes for dw
+    // alone, Deep, Twin and Many: 1024 under 1000 x 4096 (64 tiles) 47, 52 and 61 us, under 4000 x
+    // 4096 (256) 110, 104 and 97; 512 under 8000 x 1024 (128) 44, 41 and 44; 200 under 16000 x 512
+    // (126) 33, 30 and 33, under 32000 x 4096 235, 191 and 180; 100 under 8000 x 4096 67, 57 and 57,
+    // under 32000 x 4096 164, 135 and 131, under 128256 x 4096 652, 563 and 521: up to 128 rows Twin
+    // and Many are even, but under the largest vocabularies.
     if (rows <= kStepK)
         f(Tag<Outer>{});
     else if (tiles_of(vocab, 256) * tiles_of(hidden, 256) <= kCus / 2)

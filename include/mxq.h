@@ -474,7 +474,8 @@ mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t ro
  *    where they are stored.  What the rounding leaves of dz at a row's target, mostly
  *    its largest entry, is added to both sums (to dw in bf16 of its own).
  *  - A row with a target < 0 or a weight of 0 does not count: loss 0, stats
- *    (0, 1), dx 0, nothing in dw, whatever else it holds; and it costs nothing.  A
+ *    (0, 1), dx 0, nothing in dw, whatever else it holds; and it is left out of all
+ *    products, except in forward passes of up to 128 rows that are read in place.  A
  *    target >= vocab makes its row's loss and dx NaN, and dw with them.  Rows that
  *    hold NaN or infinities follow the formulas (a row whose logits hold a NaN or
  *    +inf has no distribution: S, loss and gradients NaN); the other rows' losses,
@@ -484,8 +485,9 @@ mxq_status mxq_distill(const void *logits, int32_t dtype, int64_t ld, int64_t ro
  *  - dx or dw may be NULL.  No output may overlap an input.
  * workspace: 16-byte aligned, of the size that the functions below give (0 for
  * sizes that are refused): the rows that count, packed; with them for the forward
- * pass 8 bytes for each row and 128 or 256 entries of the vocabulary, for the
- * backward pass dz of a piece (256 MiB and a part) and the sums of dx in fp32. */
+ * pass 8 bytes for each row and 64, 128 or 256 entries of the vocabulary (the fewer
+ * rows and entries, the fewer), for the backward pass dz of a piece (up to 256 MiB
+ * and a part, above 2^19 rows 512 bytes a row) and the sums of dx in fp32. */
 mxq_status mxq_linear_ce_forward(const void *x, int64_t ld_x, const void *w, int64_t ld_w,
                                  int64_t rows, int64_t hidden, int64_t vocab, float temperature,
                                  const int32_t *targets, const float *weight, float *loss,
